@@ -409,6 +409,122 @@ scape_status scape_mask_check(const scape_dims* dims, int64_t k, scape_mask_view
  */
 scape_status scape_count_nonfinite(const float* x, int64_t count, uint64_t* nonfinite_out, hipStream_t stream);
 
+/*
+ * ---- Activation checkpoints in 8 bits, and the gradient rows they give ----
+ * The operators next to the step in a training run: activations are kept in
+ * 8 bits between the forward and the backward pass, and the backward
+ * operators read them and write fp32 gradients straight into the rows of
+ * grads [K][n] that scape_step takes (a tensor's part of worker i's row
+ * starts at grads + i*n + the tensor's offset; 4-byte alignment is enough).
+ *
+ * A matrix is [rows][cols] with element (r, c) at data[r*ld + c]; ld >= cols
+ * (elements); any alignment of its element type.  A checkpoint of it is
+ *   codes   i8[rows][pitch], pitch = cols rounded up to scape_act_block()
+ *           (32); 16-byte aligned; codes past cols are written as zero
+ *   scales  u8[rows][pitch / 32]
+ * The 32 columns of a block are q * 2^(s - 127), |q| <= 127, s the scale
+ * byte.  s is the lowest >= 1 at which the block's largest magnitude is at
+ * most 127 quanta, and q rounds to nearest (ties to even), so a value is off
+ * by at most half a quantum, 1/127 of the block's largest magnitude (at the
+ * largest scale 249 codes end at 63, so that no finite value becomes infinite,
+ * and the error is at most 1.5 quanta).  s = 0:
+ * all zero.  s = 255: the block held an infinity or a NaN, and all of it
+ * reads back as NaN.  Every value has at most 8 significant bits and is
+ * exact in bf16.
+ *
+ * Limits: 0 <= rows < 2^31, 1 <= cols (in, out) <= 2^20, in * out <=
+ * 2^37, rows * ld <= 2^46.  rows = 0 reads no matrix; its pointers may then
+ * be null.  Outputs may not overlap inputs
+ * except where stated; the caller's matrices outside [rows][cols] stay as
+ * they are.  Results are deterministic.
+ */
+typedef enum { SCAPE_F32 = 0, SCAPE_BF16 = 1, SCAPE_F16 = 2 } scape_dtype;
+
+typedef struct {
+  void* data;
+  int64_t ld;
+  int32_t dtype; /* a scape_dtype */
+} scape_matrix;
+
+typedef struct {
+  int8_t* codes;
+  uint8_t* scales;
+} scape_act_view;
+
+/* Columns that share a scale (32). */
+int32_t scape_act_block(void);
+
+/* Bytes of one buffer that holds a checkpoint: the codes, then the scales,
+ * each 256-byte aligned.  0 if rows or cols is invalid. */
+size_t scape_act_bytes(int64_t rows, int64_t cols);
+
+/* The view of a checkpoint inside such a buffer (256-byte aligned device
+ * pointer).  Pure pointer arithmetic. */
+scape_status scape_act_slot(int64_t rows, int64_t cols, void* buffer, scape_act_view* out);
+
+/* out = the checkpoint of x. */
+scape_status scape_act_pack(int64_t rows, int64_t cols, scape_matrix x, scape_act_view out, hipStream_t stream);
+
+/* out = the values of a checkpoint, times gain[c] (fp32 [cols]) if gain is
+ * not null, rounded to out's type (fp16 without a gain: +-65536, to which the
+ * values next to its largest round, reads as +-65504). */
+scape_status scape_act_unpack(int64_t rows, int64_t cols, scape_act_view a, const float* gain, scape_matrix out,
+                              hipStream_t stream);
+
+/*
+ * RMS norm of a sum, with its normalised rows packed:
+ *   hs = x + residual (fp32; hs = x if residual.data is null)
+ *   rstd = fp32(1 / sqrt(mean(hs^2) + eps)), the mean in binary64
+ *   xh = hs * rstd;  y = xh * weight;  h = hs
+ * h and y are rounded to their type.  All matrices have x's type.  Outputs
+ * h, y, rstd [rows] and xhat (the checkpoint of xh, before the weight) are
+ * each left out if null, but one of y and xhat has to be there.  h or y may
+ * be x's or residual's own matrix (same data and ld).  xhat serves the
+ * norm's backward pass, and with gain = weight the weight gradients of the
+ * layers that read y.
+ */
+scape_status scape_rmsnorm_pack(int64_t rows, int64_t cols, scape_matrix x, scape_matrix residual,
+                                const float* weight, float eps, scape_matrix h, scape_matrix y, scape_act_view xhat,
+                                float* rstd, hipStream_t stream);
+
+/* Bytes of scratch scape_rmsnorm_backward needs (256-byte aligned).  0 if
+ * rows or cols is invalid. */
+size_t scape_rmsnorm_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * Backward pass of scape_rmsnorm_pack from its checkpoint: with xh the
+ * checkpoint's values and gy = dy * weight, per row
+ *   dh = rstd * (gy - xh * mean(gy * xh)) + dres
+ * (dres: the gradient that reaches h from its other reader; null: none),
+ * rounded to dh's type: the gradient of x and of residual alike.  And
+ *   dweight[c] = sum over rows of dy * xh, added to what dweight holds if
+ * accumulate is not 0.  dy, dres and dh have one type; dh may be dy's or
+ * dres's own matrix.  dh or dweight may be null (left out), not both.
+ */
+scape_status scape_rmsnorm_backward(int64_t rows, int64_t cols, scape_matrix dy, scape_act_view xhat,
+                                    const float* rstd, const float* weight, scape_matrix dres, scape_matrix dh,
+                                    float* dweight, int32_t accumulate, void* workspace, size_t workspace_bytes,
+                                    hipStream_t stream);
+
+/* Bytes of scratch scape_wgrad needs (256-byte aligned).  0 if a size is
+ * invalid. */
+size_t scape_wgrad_workspace_bytes(int64_t rows, int64_t in, int64_t out);
+
+/*
+ * Gradient of a linear layer's weight [out][in] and bias [out] from the
+ * checkpoint of its input x [rows][in] and the gradient dy [rows][out] of
+ * its output:
+ *   dw[o][i] = gain[i] * sum over rows of dy[r][o] * x[r][i]
+ *   dbias[o] = sum over rows of dy[r][o]
+ * added to what dw and dbias hold if accumulate is not 0.  gain null: 1.
+ * dbias null: left out.  dw is contiguous.  Products of a bf16 dy are exact
+ * and sums are fp32; dy of fp16 (fp32) is split into 2 (3) bf16 terms that
+ * add up to it, so nothing of it is rounded away.
+ */
+scape_status scape_wgrad(int64_t rows, int64_t in, int64_t out, scape_matrix dy, scape_act_view x, const float* gain,
+                         float* dw, float* dbias, int32_t accumulate, void* workspace, size_t workspace_bytes,
+                         hipStream_t stream);
+
 /* -------------------------------------------------------------- utility */
 
 const char* scape_status_string(scape_status s);

@@ -1,0 +1,523 @@
+// 8-bit activation checkpoints (pack, unpack) and the RMS norm with its
+// packed output, forward and backward.  All of them stream their matrices
+// once and are bound by memory; a lane owns 8 consecutive columns (a quad of
+// lanes owns the 32 columns that share a scale).
+
+#include "activations.h"
+
+namespace scape {
+namespace {
+
+// ------------------------------------------------------------ pack, unpack
+
+// A quad walks (row, block) pairs in row-major order, nquads at a time;
+// drow, dblk: nquads as rows and blocks, so that the walk needs no division.
+struct BlockWalk {
+  int64_t row;
+  int64_t blk;
+  __device__ __forceinline__ BlockWalk(int64_t quad, int64_t nblk) : row(quad / nblk), blk(quad - row * nblk) {}
+  __device__ __forceinline__ void next(int64_t drow, int64_t dblk, int64_t nblk) {
+    row += drow;
+    blk += dblk;
+    if (blk >= nblk) {
+      blk -= nblk;
+      ++row;
+    }
+  }
+};
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads)
+pack_kernel(const void* __restrict__ x, int64_t ld, int64_t rows, int64_t cols, int64_t nblk, int64_t drow,
+            int64_t dblk, int8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  const int64_t tid = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int sub = threadIdx.x & 3;
+  for (BlockWalk w(tid >> 2, nblk); w.row < rows; w.next(drow, dblk, nblk)) {
+    const int64_t c = w.blk * kActBlock + sub * 8;
+    float v[8];
+    load8<DT>(x, w.row * ld, c, cols, v);
+    const uint32_t amax = quad_max(act_amax8(v));
+    uint32_t s;
+    const u32x2 q = act_encode(v, amax, &s);
+    const int64_t b = w.row * nblk + w.blk;
+    *reinterpret_cast<u32x2*>(codes + b * kActBlock + sub * 8) = q;
+    if (sub == 0) scales[b] = (uint8_t)s;
+  }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads)
+unpack_kernel(const int8_t* __restrict__ codes, const uint8_t* __restrict__ scales, const float* __restrict__ gain,
+              int64_t rows, int64_t cols, int64_t nblk, int64_t drow, int64_t dblk, void* __restrict__ out,
+              int64_t ld) {
+  const int64_t tid = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int sub = threadIdx.x & 3;
+  for (BlockWalk w(tid >> 2, nblk); w.row < rows; w.next(drow, dblk, nblk)) {
+    const int64_t b = w.row * nblk + w.blk;
+    const int64_t c = w.blk * kActBlock + sub * 8;
+    float v[8];
+    act_decode(*reinterpret_cast<const u32x2*>(codes + b * kActBlock + sub * 8), scales[b], v);
+    if (gain) {
+      float g[8];
+      load8<SCAPE_F32>(gain, 0, c, cols, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= g[j];
+    } else if (DT == SCAPE_F16) {  // 64 quanta of 2^10 are past the type's range, the packed value was not
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __builtin_fabsf(v[j]) == 65536.0f ? __builtin_copysignf(65504.0f, v[j]) : v[j];
+    }
+    store8<DT>(out, w.row * ld, c, cols, v);
+  }
+}
+
+unsigned walk_grid(int64_t rows, int64_t nblk) {
+  const int64_t need = (rows * nblk * 4 + kThreads - 1) / kThreads;
+  return (unsigned)(need > 16384 ? 16384 : need);
+}
+
+// ---------------------------------------------------------------- RMS norm
+
+// Sum over the T threads (64: a wave; 256: the workgroup) that share a row;
+// every thread gets it, the same one.
+template <typename V>
+__device__ __forceinline__ V wave_sum(V x) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d, 64);
+  return x;
+}
+template <int T, typename V>
+__device__ __forceinline__ V row_sum(V x, V* lds) {
+  x = wave_sum(x);
+  if (T == 64) return x;
+  __syncthreads();  // the previous row's sum has been read
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
+  __syncthreads();
+  return ((lds[0] + lds[1]) + lds[2]) + lds[3];
+}
+
+struct NormArgs {
+  int64_t rows, cols, nblk;
+  const void* x;
+  int64_t x_ld;
+  const void* res;
+  int64_t res_ld;
+  const float* weight;
+  float eps;
+  void* h;
+  int64_t h_ld;
+  void* y;
+  int64_t y_ld;
+  int8_t* codes;
+  uint8_t* scales;
+  float* rstd;
+};
+
+template <int DT>
+__device__ __forceinline__ void load_sum(const NormArgs& a, int64_t row, int64_t c, float (&v)[8]) {
+  load8<DT>(a.x, row * a.x_ld, c, a.cols, v);
+  if (a.res) {
+    float r[8];
+    load8<DT>(a.res, row * a.res_ld, c, a.cols, r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += r[j];
+  }
+}
+
+// h, y and the code of one lane's 8 columns (a quad writes one scale).
+template <int DT>
+__device__ __forceinline__ void norm_emit(const NormArgs& a, int64_t row, int64_t c, const float (&v)[8], float rs) {
+  if (a.h && c < a.cols) store8<DT>(a.h, row * a.h_ld, c, a.cols, v);
+  float xh[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) xh[j] = v[j] * rs;
+  if (a.y && c < a.cols) {
+    float w[8];
+    load8<SCAPE_F32>(a.weight, 0, c, a.cols, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = xh[j] * w[j];
+    store8<DT>(a.y, row * a.y_ld, c, a.cols, w);
+  }
+  if (a.codes) {
+    const uint32_t amax = quad_max(act_amax8(xh));
+    uint32_t s;
+    const u32x2 q = act_encode(xh, amax, &s);
+    if (c < a.nblk * kActBlock) {
+      const int64_t b = row * a.nblk + c / kActBlock;
+      *reinterpret_cast<u32x2*>(a.codes + b * kActBlock + (c & 31)) = q;
+      if ((threadIdx.x & 3) == 0) a.scales[b] = (uint8_t)s;
+    }
+  }
+}
+
+// The reciprocal RMS.  Binary64, so that rstd (and with it every code, which
+// a last-bit change of rstd could move across a rounding border) does not
+// depend on how many threads share a row.
+__device__ __forceinline__ float norm_rstd(double sum, int64_t cols, float eps) {
+  return (float)(1.0 / sqrt(sum / (double)cols + (double)eps));
+}
+
+// Rows held in registers: T threads a row, C chunks of 8 columns a thread
+// (T * C * 8 >= cols).
+template <int DT, int T, int C>
+__global__ void __launch_bounds__(kThreads) norm_kernel(NormArgs a) {
+  __shared__ double lds[4];
+  constexpr int kRows = kThreads / T;
+  const int t = threadIdx.x % T;
+  for (int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / T; row < a.rows; row += (int64_t)gridDim.x * kRows) {
+    float v[C][8];
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      load_sum<DT>(a, row, (int64_t)(i * T + t) * 8, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s = fma((double)v[i][j], (double)v[i][j], s);
+    s = row_sum<T>(s, lds);
+    const float rs = norm_rstd(s, a.cols, a.eps);
+    if (a.rstd && t == 0) a.rstd[row] = rs;
+#pragma unroll
+    for (int i = 0; i < C; ++i) norm_emit<DT>(a, row, (int64_t)(i * T + t) * 8, v[i], rs);
+  }
+}
+
+// Rows too long for registers: one workgroup a row, two passes over it.
+// h and y may be x's or residual's matrix: nothing is written before every
+// thread has summed, and then each thread reads what it overwrites first.
+template <int DT>
+__global__ void __launch_bounds__(kThreads) norm_long_kernel(NormArgs a) {
+  __shared__ double lds[4];
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    double s = 0.0;
+    for (int64_t c = (int64_t)threadIdx.x * 8; c < a.cols; c += kThreads * 8) {
+      float v[8];
+      load_sum<DT>(a, row, c, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s = fma((double)v[j], (double)v[j], s);
+    }
+    s = row_sum<kThreads>(s, lds);
+    const float rs = norm_rstd(s, a.cols, a.eps);
+    if (a.rstd && threadIdx.x == 0) a.rstd[row] = rs;
+    // whole quads walk to the end of the last block
+    for (int64_t c = (int64_t)threadIdx.x * 8; c < a.nblk * kActBlock; c += kThreads * 8) {
+      float v[8];
+      load_sum<DT>(a, row, c, v);
+      norm_emit<DT>(a, row, c, v, rs);
+    }
+  }
+}
+
+struct NormBackArgs {
+  int64_t rows, cols, nblk;
+  const void* dy;
+  int64_t dy_ld;
+  const int8_t* codes;
+  const uint8_t* scales;
+  const float* rstd;
+  const float* weight;
+  const void* dres;
+  int64_t dres_ld;
+  void* dh;
+  int64_t dh_ld;
+  float* dw;  // [gridDim.x][cols] partial sums, or dweight itself (one block)
+  bool accumulate;
+};
+
+__device__ __forceinline__ void load_hat(const NormBackArgs& a, int64_t row, int64_t c, float (&v)[8]) {
+  if (c < a.nblk * kActBlock) {
+    const int64_t b = row * a.nblk + c / kActBlock;
+    act_decode(*reinterpret_cast<const u32x2*>(a.codes + b * kActBlock + (c & 31)), a.scales[b], v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+  }
+}
+
+// dh of one lane's 8 columns, from g = dy * weight and c = mean(g * xh).
+template <int DT>
+__device__ __forceinline__ void back_emit(const NormBackArgs& a, int64_t row, int64_t c, const float (&g)[8],
+                                          const float (&xh)[8], float mean, float rs) {
+  if (c >= a.cols) return;
+  float o[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = rs * (g[j] - xh[j] * mean);
+  if (a.dres) {
+    float r[8];
+    load8<DT>(a.dres, row * a.dres_ld, c, a.cols, r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] += r[j];
+  }
+  store8<DT>(a.dh, row * a.dh_ld, c, a.cols, o);
+}
+
+template <int DT, int T, int C>
+__global__ void __launch_bounds__(kThreads) norm_back_kernel(NormBackArgs a) {
+  __shared__ float lds[4];
+  __shared__ float part[T == 64 ? 64 * C * 8 : 1];
+  constexpr int kRows = kThreads / T;
+  const int t = threadIdx.x % T;
+  float dw[C][8];
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+  for (int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / T; row < a.rows; row += (int64_t)gridDim.x * kRows) {
+    float g[C][8], xh[C][8];
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int64_t c = (int64_t)(i * T + t) * 8;
+      load8<DT>(a.dy, row * a.dy_ld, c, a.cols, g[i]);
+      load_hat(a, row, c, xh[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float w[8];
+      load8<SCAPE_F32>(a.weight, 0, (int64_t)(i * T + t) * 8, a.cols, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dw[i][j] = __builtin_fmaf(g[i][j], xh[i][j], dw[i][j]);
+        g[i][j] *= w[j];
+        sum = __builtin_fmaf(g[i][j], xh[i][j], sum);
+      }
+    }
+    if (a.dh) {
+      const float mean = row_sum<T>(sum, lds) / (float)a.cols;
+      const float rs = a.rstd[row];
+#pragma unroll
+      for (int i = 0; i < C; ++i) back_emit<DT>(a, row, (int64_t)(i * T + t) * 8, g[i], xh[i], mean, rs);
+    }
+  }
+  if (!a.dw) return;
+  if (T == 64) {  // the four waves' sums, in wave order
+    for (int w = 0; w < 4; ++w) {
+      if (threadIdx.x / 64 == w) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float* p = &part[(i * 8 + j) * 64 + t];
+            *p = w == 0 ? dw[i][j] : *p + dw[i][j];
+            dw[i][j] = *p;
+          }
+      }
+      __syncthreads();
+    }
+    if (threadIdx.x / 64 != 3) return;
+  }
+  float* out = a.dw + (int64_t)blockIdx.x * a.cols;
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int64_t c = (int64_t)(i * T + t) * 8;
+    if (c >= a.cols) continue;
+    if (a.accumulate) {
+      float o[8];
+      load8<SCAPE_F32>(out, 0, c, a.cols, o);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) dw[i][j] += o[j];
+    }
+    store8<SCAPE_F32>(out, 0, c, a.cols, dw[i]);
+  }
+}
+
+// Long rows: dweight first (dh may overwrite dy), then dh in two passes a row.
+template <int DT>
+__global__ void __launch_bounds__(kThreads) norm_back_long_dw_kernel(NormBackArgs a) {
+  const int64_t c = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * 8;
+  if (c >= a.cols) return;
+  float dw[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    float g[8], xh[8];
+    load8<DT>(a.dy, row * a.dy_ld, c, a.cols, g);
+    load_hat(a, row, c, xh);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[j] = __builtin_fmaf(g[j], xh[j], dw[j]);
+  }
+  float* out = a.dw + (int64_t)blockIdx.x * a.cols;
+  if (a.accumulate) {
+    float o[8];
+    load8<SCAPE_F32>(out, 0, c, a.cols, o);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[j] += o[j];
+  }
+  store8<SCAPE_F32>(out, 0, c, a.cols, dw);
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads) norm_back_long_kernel(NormBackArgs a) {
+  __shared__ float lds[4];
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    float sum = 0.0f;
+    for (int64_t c = (int64_t)threadIdx.x * 8; c < a.cols; c += kThreads * 8) {
+      float g[8], xh[8], w[8];
+      load8<DT>(a.dy, row * a.dy_ld, c, a.cols, g);
+      load_hat(a, row, c, xh);
+      load8<SCAPE_F32>(a.weight, 0, c, a.cols, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(g[j] * w[j], xh[j], sum);
+    }
+    const float mean = row_sum<kThreads>(sum, lds) / (float)a.cols;
+    const float rs = a.rstd[row];
+    for (int64_t c = (int64_t)threadIdx.x * 8; c < a.cols; c += kThreads * 8) {
+      float g[8], xh[8], w[8];
+      load8<DT>(a.dy, row * a.dy_ld, c, a.cols, g);
+      load_hat(a, row, c, xh);
+      load8<SCAPE_F32>(a.weight, 0, c, a.cols, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] *= w[j];
+      back_emit<DT>(a, row, c, g, xh, mean, rs);
+    }
+  }
+}
+
+// out[c] (+)= the sum of parts[0 .. n)[c], 4 groups of parts a column, each
+// in order, then the groups in order.
+__global__ void __launch_bounds__(kThreads)
+sum_parts_kernel(const float* __restrict__ parts, int64_t n, int64_t cols, float* __restrict__ out, bool accumulate) {
+  __shared__ float lds[4][64];
+  const int lane = threadIdx.x & 63, grp = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  float s = 0.0f;
+  if (c < cols)
+    for (int64_t p = grp; p < n; p += 4) s += parts[p * cols + c];
+  lds[grp][lane] = s;
+  __syncthreads();
+  if (grp == 0 && c < cols) {
+    s = ((lds[0][lane] + lds[1][lane]) + lds[2][lane]) + lds[3][lane];
+    out[c] = accumulate ? out[c] + s : s;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) zero_f32_kernel(float* p, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i < n) p[i] = 0.0f;
+}
+
+constexpr int64_t kWaveCols = 64 * 8 * 8;    // longest row one wave holds
+constexpr int64_t kGroupCols = 256 * 8 * 8;  // longest row one workgroup holds
+constexpr int64_t kBackBlocks = 512;
+
+template <int DT, int T>
+void norm_chunks(const NormArgs& a, unsigned grid, int64_t chunks, hipStream_t s) {
+  switch (chunks) {
+#define CASE(C) \
+  case C: norm_kernel<DT, T, C><<<grid, kThreads, 0, s>>>(a); break;
+    CASE(1) CASE(2) CASE(3) CASE(4) CASE(5) CASE(6) CASE(7) CASE(8)
+#undef CASE
+  }
+}
+
+template <int DT, int T>
+void back_chunks(const NormBackArgs& a, unsigned grid, int64_t chunks, hipStream_t s) {
+  switch (chunks) {
+#define CASE(C) \
+  case C: norm_back_kernel<DT, T, C><<<grid, kThreads, 0, s>>>(a); break;
+    CASE(1) CASE(2) CASE(3) CASE(4) CASE(5) CASE(6) CASE(7) CASE(8)
+#undef CASE
+  }
+}
+
+unsigned cap_grid(int64_t need, int64_t most) { return (unsigned)(need < most ? need : most); }
+
+template <int DT>
+void norm_launch(const NormArgs& a, hipStream_t s) {
+  if (a.cols <= kWaveCols)
+    norm_chunks<DT, 64>(a, cap_grid((a.rows + 3) / 4, 65536), (a.cols + 511) / 512, s);
+  else if (a.cols <= kGroupCols)
+    norm_chunks<DT, 256>(a, cap_grid(a.rows, 65536), (a.cols + 2047) / 2048, s);
+  else
+    norm_long_kernel<DT><<<cap_grid(a.rows, 65536), kThreads, 0, s>>>(a);
+}
+
+template <int DT>
+void back_launch(const NormBackArgs& a, unsigned parts, hipStream_t s) {
+  if (a.cols <= kWaveCols) {
+    back_chunks<DT, 64>(a, parts, (a.cols + 511) / 512, s);
+  } else if (a.cols <= kGroupCols) {
+    back_chunks<DT, 256>(a, parts, (a.cols + 2047) / 2048, s);
+  } else {
+    if (a.dw)
+      norm_back_long_dw_kernel<DT><<<dim3(parts, (unsigned)((a.cols + 2047) / 2048)), kThreads, 0, s>>>(a);
+    if (a.dh) norm_back_long_kernel<DT><<<cap_grid(a.rows, 65536), kThreads, 0, s>>>(a);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_act_pack(int64_t rows, int64_t cols, const scape_matrix& x, const scape_act_view& out,
+                           hipStream_t s) {
+  if (rows < 1) return hipSuccess;
+  const int64_t nblk = act_blocks(cols);
+  const unsigned grid = walk_grid(rows, nblk);
+  const int64_t quads = (int64_t)grid * kThreads / 4;
+  const int64_t drow = quads / nblk, dblk = quads % nblk;
+#define PACK(DT) \
+  case DT: pack_kernel<DT><<<grid, kThreads, 0, s>>>(x.data, x.ld, rows, cols, nblk, drow, dblk, out.codes, out.scales); break;
+  switch (x.dtype) { PACK(SCAPE_F32) PACK(SCAPE_BF16) PACK(SCAPE_F16) }
+#undef PACK
+  return hipGetLastError();
+}
+
+hipError_t launch_act_unpack(int64_t rows, int64_t cols, const scape_act_view& a, const float* gain,
+                             const scape_matrix& out, hipStream_t s) {
+  if (rows < 1) return hipSuccess;
+  const int64_t nblk = act_blocks(cols);
+  const unsigned grid = walk_grid(rows, nblk);
+  const int64_t quads = (int64_t)grid * kThreads / 4;
+  const int64_t drow = quads / nblk, dblk = quads % nblk;
+#define UNPACK(DT) \
+  case DT: unpack_kernel<DT><<<grid, kThreads, 0, s>>>(a.codes, a.scales, gain, rows, cols, nblk, drow, dblk, out.data, out.ld); break;
+  switch (out.dtype) { UNPACK(SCAPE_F32) UNPACK(SCAPE_BF16) UNPACK(SCAPE_F16) }
+#undef UNPACK
+  return hipGetLastError();
+}
+
+hipError_t launch_rmsnorm_pack(int64_t rows, int64_t cols, const scape_matrix& x, const scape_matrix& residual,
+                               const float* weight, float eps, const scape_matrix& h, const scape_matrix& y,
+                               const scape_act_view& xhat, float* rstd, hipStream_t s) {
+  if (rows < 1) return hipSuccess;
+  NormArgs a{rows, cols, act_blocks(cols), x.data, x.ld, residual.data, residual.ld, weight, eps,
+             h.data, h.ld, y.data, y.ld, xhat.codes, xhat.scales, rstd};
+  switch (x.dtype) {
+    case SCAPE_F32: norm_launch<SCAPE_F32>(a, s); break;
+    case SCAPE_BF16: norm_launch<SCAPE_BF16>(a, s); break;
+    case SCAPE_F16: norm_launch<SCAPE_F16>(a, s); break;
+  }
+  return hipGetLastError();
+}
+
+int64_t rmsnorm_parts(int64_t rows, int64_t cols) {
+  const int64_t per = cols <= kWaveCols ? 4 : 1;  // rows a workgroup works on at a time
+  const int64_t need = (rows + per - 1) / per;
+  return need < 1 ? 1 : (need < kBackBlocks ? need : kBackBlocks);
+}
+
+hipError_t launch_rmsnorm_backward(int64_t rows, int64_t cols, const scape_matrix& dy, const scape_act_view& xhat,
+                                   const float* rstd, const float* weight, const scape_matrix& dres,
+                                   const scape_matrix& dh, float* dweight, bool accumulate, float* parts,
+                                   hipStream_t s) {
+  if (rows < 1) {
+    if (dweight && !accumulate)
+      zero_f32_kernel<<<(unsigned)((cols + kThreads - 1) / kThreads), kThreads, 0, s>>>(dweight, cols);
+    return hipGetLastError();
+  }
+  const int64_t n = rmsnorm_parts(rows, cols);
+  NormBackArgs a{rows, cols, act_blocks(cols), dy.data, dy.ld, xhat.codes, xhat.scales, rstd, weight,
+                 dres.data, dres.ld, dh.data, dh.ld, nullptr, false};
+  if (dweight) {
+    a.dw = n == 1 ? dweight : parts;
+    a.accumulate = n == 1 && accumulate;
+  }
+  switch (dy.dtype) {
+    case SCAPE_F32: back_launch<SCAPE_F32>(a, (unsigned)n, s); break;
+    case SCAPE_BF16: back_launch<SCAPE_BF16>(a, (unsigned)n, s); break;
+    case SCAPE_F16: back_launch<SCAPE_F16>(a, (unsigned)n, s); break;
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !dweight || n == 1) return e;
+  sum_parts_kernel<<<(unsigned)((cols + 63) / 64), kThreads, 0, s>>>(parts, n, cols, dweight, accumulate);
+  return hipGetLastError();
+}
+
+}  // namespace scape

@@ -94,9 +94,9 @@ bool make_geom(int64_t n, int P, int K, int64_t k, Geom* g) {
 
 using namespace scape;
 
-namespace {
+namespace scape {
 
-thread_local char g_err[512] = "";
+static thread_local char g_err[512] = "";
 
 scape_status fail(scape_status s, const char* fmt, ...) {
   va_list ap;
@@ -110,6 +110,10 @@ scape_status hip_check(hipError_t e, const char* where) {
   if (e != hipSuccess) return fail(SCAPE_EHIP, "%s: %s", where, hipGetErrorString(e));
   return SCAPE_OK;
 }
+
+}  // namespace scape
+
+namespace {
 
 scape_status check_dims(const scape_dims* d, int64_t k, Geom* g) {
   if (!d) return fail(SCAPE_EINVAL, "dims is null");

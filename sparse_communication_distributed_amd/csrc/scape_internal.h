@@ -10,6 +10,11 @@
 
 namespace scape {
 
+// Records the detail of a failing call (scape_last_error) and returns s.
+scape_status fail(scape_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+// SCAPE_EHIP with the HIP error's text, or SCAPE_OK.
+scape_status hip_check(hipError_t e, const char* where);
+
 // Compaction / work tile: 4096 elements = 64 mask words.
 constexpr int64_t kTile = 4096;
 constexpr int kWordsPerTile = 64;

@@ -40,6 +40,16 @@ class BiasState(ctypes.Structure):
     _fields_ = [("beta1_pow", ctypes.c_double), ("beta2_pow", ctypes.c_double), ("ibc1", c_float), ("ibc2", c_float)]
 
 
+class Matrix(ctypes.Structure):
+    """scape_matrix: rows ld elements apart, of one of the scape_dtype types."""
+    _fields_ = [("data", c_void_p), ("ld", c_int64), ("dtype", c_int32)]
+
+
+class ActView(ctypes.Structure):
+    """scape_act_view: codes and scale bytes of an 8-bit checkpoint."""
+    _fields_ = [("codes", c_void_p), ("scales", c_void_p)]
+
+
 class ScapeError(RuntimeError):
     def __init__(self, status: int, detail: str):
         self.status = status
@@ -84,6 +94,19 @@ _SIGS = {
                                      c_void_p, Betas, c_int64, c_void_p, c_size_t, c_void_p]),
     "scape_shard_update": (c_int, [ctypes.POINTER(Dims), c_int64, c_int32, c_void_p, c_void_p, c_void_p, c_void_p,
                                    c_void_p, Betas, c_float, c_int64, c_void_p]),
+    "scape_act_block": (c_int32, []),
+    "scape_act_bytes": (c_size_t, [c_int64, c_int64]),
+    "scape_act_slot": (c_int, [c_int64, c_int64, c_void_p, ctypes.POINTER(ActView)]),
+    "scape_act_pack": (c_int, [c_int64, c_int64, Matrix, ActView, c_void_p]),
+    "scape_act_unpack": (c_int, [c_int64, c_int64, ActView, c_void_p, Matrix, c_void_p]),
+    "scape_rmsnorm_pack": (c_int, [c_int64, c_int64, Matrix, Matrix, c_void_p, c_float, Matrix, Matrix, ActView,
+                                   c_void_p, c_void_p]),
+    "scape_rmsnorm_workspace_bytes": (c_size_t, [c_int64, c_int64]),
+    "scape_rmsnorm_backward": (c_int, [c_int64, c_int64, Matrix, ActView, c_void_p, c_void_p, Matrix, Matrix,
+                                       c_void_p, c_int32, c_void_p, c_size_t, c_void_p]),
+    "scape_wgrad_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64]),
+    "scape_wgrad": (c_int, [c_int64, c_int64, c_int64, Matrix, ActView, c_void_p, c_void_p, c_void_p, c_int32,
+                            c_void_p, c_size_t, c_void_p]),
     "scape_status_string": (c_char_p, [c_int]),
     "scape_last_error": (c_char_p, []),
     "scape_profile_stages": (c_int, []),
@@ -418,6 +441,220 @@ def count_nonfinite(x, count_out, count=None, stream=None) -> None:
 def mask_overlap(d: Dims, k: int, a: MaskView, b: MaskView, count_out, stream=None) -> None:
     _need(count_out, "count_out", 8, dtype=None)
     _check(lib().scape_mask_overlap(ctypes.byref(d), k, a, b, _ptr(count_out), _stream(stream)))
+
+
+# ------------------------------------- 8-bit activations, gradient rows
+
+ACT_BLOCK = 32  # columns that share a scale (scape_act_block)
+
+
+class ActCheckpoint:
+    """An 8-bit activation checkpoint of a [rows][cols] matrix: ``codes``
+    (int8 [rows][pitch], pitch = cols rounded up to 32) and ``scales`` (uint8
+    [rows][pitch / 32]), contiguous tensors on one device."""
+
+    __slots__ = ("codes", "scales", "rows", "cols", "device", "view")
+
+    def __init__(self, codes, scales, cols: int):
+        import torch
+        self.codes, self.scales, self.cols = codes, scales, int(cols)
+        nb = (self.cols + ACT_BLOCK - 1) // ACT_BLOCK
+        if codes.dim() != 2 or scales.dim() != 2 or codes.dtype != torch.int8 or scales.dtype != torch.uint8:
+            raise ValueError("codes must be int8 [rows][pitch] and scales uint8 [rows][pitch / 32]")
+        self.rows = codes.shape[0]
+        if self.cols < 1 or tuple(codes.shape) != (self.rows, nb * ACT_BLOCK) or tuple(scales.shape) != (self.rows, nb):
+            raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} do not fit {self.cols} columns")
+        if not (codes.is_contiguous() and scales.is_contiguous()):
+            raise ValueError("codes and scales must be contiguous")
+        if not codes.is_cuda or scales.device != codes.device:
+            raise ValueError("codes and scales must be device tensors of one device")
+        self.device = codes.get_device()
+        self.view = ActView(codes.data_ptr(), scales.data_ptr())
+
+
+def act_bytes(rows: int, cols: int) -> int:
+    return int(lib().scape_act_bytes(rows, cols))
+
+
+def act_in(buffer, rows: int, cols: int) -> ActCheckpoint:
+    """The checkpoint that lies inside `buffer`, a uint8 device tensor of at
+    least act_bytes(rows, cols) bytes (256-byte aligned)."""
+    import torch
+    need = act_bytes(rows, cols)
+    if need == 0:
+        raise ScapeError(2, f"invalid shape rows={rows} cols={cols}")
+    _need(buffer, "buffer", need, dtype="uint8")
+    if buffer.data_ptr() % 256:
+        raise ValueError("buffer must be 256-byte aligned")
+    mv = ActView()
+    _check(lib().scape_act_slot(rows, cols, buffer.data_ptr(), ctypes.byref(mv)))
+    nb = (cols + ACT_BLOCK - 1) // ACT_BLOCK
+    off = mv.scales - buffer.data_ptr()
+    flat = buffer.view(-1)
+    return ActCheckpoint(flat[:rows * nb * ACT_BLOCK].view(torch.int8).view(rows, nb * ACT_BLOCK),
+                         flat[off:off + rows * nb].view(rows, nb), cols)
+
+
+def act_alloc(rows: int, cols: int, device) -> ActCheckpoint:
+    """A new checkpoint (contents undefined until packed)."""
+    import torch
+    need = act_bytes(rows, cols)
+    if need == 0:
+        raise ScapeError(2, f"invalid shape rows={rows} cols={cols}")
+    return act_in(torch.empty(need, dtype=torch.uint8, device=device), rows, cols)
+
+
+_NO_MATRIX = Matrix(None, 0, 0)
+_NO_ACT = ActView(None, None)
+_DTYPES = None
+
+
+def _matrix(t, name: str, rows: int, cols: int, device: int) -> Matrix:
+    """A [rows][cols] device tensor of fp32, bf16 or fp16 with consecutive
+    elements in a row and rows that do not overlap; None: no matrix."""
+    global _DTYPES
+    if t is None:
+        return _NO_MATRIX
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    if t.get_device() != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a tensor on device {device} (got {t.device})")
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16 (got {t.dtype})")
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} must have shape ({rows}, {cols}) (got {tuple(t.shape)})")
+    ld, one = t.stride()
+    if cols > 1 and one != 1:
+        raise ValueError(f"{name} must have consecutive elements in a row (stride {one})")
+    if rows < 2:
+        ld = cols
+    elif ld < cols:
+        raise ValueError(f"{name}: rows {ld} elements apart overlap (cols {cols})")
+    return Matrix(t.data_ptr(), ld, dt)
+
+
+def _vector(t, name: str, numel: int, device: int) -> Optional[int]:
+    """Address of a contiguous fp32 device tensor of `numel` elements."""
+    if t is None:
+        return None
+    import torch
+    if t.get_device() != device or not t.is_cuda or t.dtype != torch.float32:
+        raise ValueError(f"{name} must be a float32 tensor on device {device} (got {t.dtype} on {t.device})")
+    if not t.is_contiguous() or t.numel() != numel:
+        raise ValueError(f"{name} must be contiguous with {numel} elements (got {tuple(t.shape)})")
+    return t.data_ptr()
+
+
+def _act(a, name: str, rows: int, cols: int, device: int) -> ActView:
+    if a is None:
+        return _NO_ACT
+    if a.device != device or a.rows != rows or a.cols != cols:
+        raise ValueError(f"{name} must be a checkpoint of ({rows}, {cols}) on device {device} "
+                         f"(got ({a.rows}, {a.cols}) on device {a.device})")
+    return a.view
+
+
+def _workspace(t, need: int, device: int):
+    if t.get_device() != device or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on device {device}")
+    have = t.numel() * t.element_size()
+    if have < need:
+        raise ValueError(f"workspace is too small: {have} bytes, needs {need}")
+    if t.data_ptr() % 256:
+        raise ValueError("workspace must be 256-byte aligned")
+    return t.data_ptr(), have
+
+
+def _device_of(t, name: str) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor (got {t.device})")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions (got {tuple(t.shape)})")
+    return t.get_device()
+
+
+def _enqueue(device: int, stream, fn, *args) -> None:
+    """Calls fn(*args, stream) with `device` current: on the given stream,
+    which has to be that device's, or on the device's current one."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device.index != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on device {device}")
+    if torch.cuda.current_device() == device:
+        _check(fn(*args, stream.cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, stream.cuda_stream))
+
+
+def act_pack(x, out: ActCheckpoint, stream=None) -> None:
+    """out = the 8-bit checkpoint of x [rows][cols]."""
+    dev = _device_of(x, "x")
+    rows, cols = x.shape
+    _enqueue(dev, stream, lib().scape_act_pack, rows, cols, _matrix(x, "x", rows, cols, dev),
+             _act(out, "out", rows, cols, dev))
+
+
+def act_unpack(a: ActCheckpoint, out, gain=None, stream=None) -> None:
+    """out [rows][cols] = the checkpoint's values (times gain[cols])."""
+    dev, rows, cols = a.device, a.rows, a.cols
+    _enqueue(dev, stream, lib().scape_act_unpack, rows, cols, a.view, _vector(gain, "gain", cols, dev),
+             _matrix(out, "out", rows, cols, dev))
+
+
+def rmsnorm_pack(x, weight, eps: float, y=None, xhat: Optional[ActCheckpoint] = None, rstd=None, residual=None,
+                 h=None, stream=None) -> None:
+    """RMS norm of x + residual: y (times weight), the sum h, the reciprocal
+    RMS rstd [rows], and xhat, the 8-bit checkpoint of the normalised rows
+    before the weight.  Outputs that are None are left out."""
+    dev = _device_of(x, "x")
+    rows, cols = x.shape
+    _enqueue(dev, stream, lib().scape_rmsnorm_pack, rows, cols, _matrix(x, "x", rows, cols, dev),
+             _matrix(residual, "residual", rows, cols, dev), _vector(weight, "weight", cols, dev), eps,
+             _matrix(h, "h", rows, cols, dev), _matrix(y, "y", rows, cols, dev), _act(xhat, "xhat", rows, cols, dev),
+             _vector(rstd, "rstd", rows, dev))
+
+
+def rmsnorm_workspace_bytes(rows: int, cols: int) -> int:
+    return int(lib().scape_rmsnorm_workspace_bytes(rows, cols))
+
+
+def rmsnorm_backward(dy, xhat: ActCheckpoint, rstd, weight, dh, dweight, workspace, dres=None,
+                     accumulate: bool = False, stream=None) -> None:
+    """Backward pass of rmsnorm_pack from its checkpoint: dh [rows][cols]
+    (the gradient of x and of residual) and dweight [cols], set or (with
+    accumulate) added to.  dres: the gradient that reaches h directly."""
+    dev = _device_of(dy, "dy")
+    rows, cols = dy.shape
+    ws, have = _workspace(workspace, rmsnorm_workspace_bytes(rows, cols), dev)
+    _enqueue(dev, stream, lib().scape_rmsnorm_backward, rows, cols, _matrix(dy, "dy", rows, cols, dev),
+             _act(xhat, "xhat", rows, cols, dev), _vector(rstd, "rstd", rows, dev),
+             _vector(weight, "weight", cols, dev), _matrix(dres, "dres", rows, cols, dev),
+             _matrix(dh, "dh", rows, cols, dev), _vector(dweight, "dweight", cols, dev), 1 if accumulate else 0,
+             ws, have)
+
+
+def wgrad_workspace_bytes(rows: int, n_in: int, n_out: int) -> int:
+    return int(lib().scape_wgrad_workspace_bytes(rows, n_in, n_out))
+
+
+def wgrad(dy, x: ActCheckpoint, dw, workspace, gain=None, dbias=None, accumulate: bool = False, stream=None) -> None:
+    """Weight gradient dw [out][in] (and dbias [out]) of a linear layer from
+    the gradient dy [rows][out] of its output and the checkpoint x [rows][in]
+    of its input (times gain[in]); set or (with accumulate) added to.  dw and
+    dbias may be parts of a row of the optimizer's gradients."""
+    dev = _device_of(dy, "dy")
+    rows, n_out = dy.shape
+    n_in = x.cols
+    ws, have = _workspace(workspace, wgrad_workspace_bytes(rows, n_in, n_out), dev)
+    if dw is None:
+        raise ValueError("dw is needed")
+    _enqueue(dev, stream, lib().scape_wgrad, rows, n_in, n_out, _matrix(dy, "dy", rows, n_out, dev),
+             _act(x, "x", rows, n_in, dev), _vector(gain, "gain", n_in, dev), _vector(dw, "dw", n_out * n_in, dev),
+             _vector(dbias, "dbias", n_out, dev), 1 if accumulate else 0, ws, have)
 
 
 # ---------------------------------------------------------------- profiling

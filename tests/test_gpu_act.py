@@ -1,0 +1,599 @@
+"""The activation operators on the GPU against the oracle: codes, scales and
+rstd exactly, the rest within bounds counted from the roundings of each
+formula (u = 2^-24 for a 32-bit operation, half an epsilon for the final
+rounding to the output's type)."""
+
+import numpy as np
+import pytest
+
+from oracle import act_oracle as A
+
+torch = pytest.importorskip("torch")
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
+
+DEV = "cuda:0"
+U = 2.0 ** -24
+EPS = 1e-5
+DT = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}
+HALF = {t: torch.finfo(t).eps / 2 for t in DT.values()}
+# half of the spacing of the type's subnormal numbers: what rounding loses there
+LEAST = {torch.float32: 2.0 ** -150, torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25}
+
+
+@pytest.fixture(scope="module")
+def S():
+    from sparse_communication_distributed_amd import scape
+    scape.lib()
+    return scape
+
+
+def spread(rows, cols, seed, scale=1.0):
+    """Values over several magnitudes, some rows and some blocks all zero."""
+    r = np.random.default_rng(seed)
+    x = r.standard_normal((rows, cols)) * np.exp(1.5 * r.standard_normal((rows, 1))) * scale
+    x[r.random(rows) < 0.1] = 0.0
+    x[:, : cols // 3][r.random((rows, cols // 3)) < 0.3] = 0.0
+    return x
+
+
+class Guarded:
+    """A [rows][cols] matrix inside a larger buffer of sentinels."""
+
+    def __init__(self, rows, cols, dtype, pad=0, lead=0, fill=None):
+        ld = cols + pad
+        self.buf = torch.full((rows * ld + lead + 64,), -77.0, dtype=dtype, device=DEV)
+        self.t = self.buf[lead:lead + rows * ld].view(rows, ld)[:, :cols]
+        self.lead, self.rows, self.ld = lead, rows, ld
+        if fill is not None:
+            self.t.copy_(torch.from_numpy(np.asarray(fill)))
+
+    def check(self):
+        rest = self.buf.clone()
+        rest[self.lead:self.lead + self.rows * self.ld].view(self.rows, self.ld)[:, :self.t.shape[1]] = -77.0
+        assert (rest == -77.0).all(), "written outside the matrix"
+
+
+def f32(t):
+    return t.float().cpu().numpy()
+
+
+def codes_of(a):
+    return a.codes.cpu().numpy(), a.scales.cpu().numpy()
+
+
+def fill_act(S, codes, scales, cols):
+    return S.ActCheckpoint(torch.from_numpy(codes).to(DEV), torch.from_numpy(scales).to(DEV), cols)
+
+
+def within(got, want, tol, name):
+    got = got.double().cpu().numpy() if torch.is_tensor(got) else got
+    bad = ~(np.abs(got - want) <= tol)
+    if bad.any():
+        i = tuple(np.argwhere(bad)[0])
+        raise AssertionError(f"{name}: {int(bad.sum())} of {bad.size} beyond the bound; first {i}: got {got[i]!r} "
+                             f"want {want[i]!r} tolerance {np.broadcast_to(tol, bad.shape)[i]!r}")
+
+
+# ------------------------------------------------------------ pack, unpack
+
+SHAPES = [(1, 1), (3, 31), (5, 33), (2, 32), (7, 777), (33, 1280), (1, 5632), (130, 64), (1, 70001)]
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("rows,cols", SHAPES)
+def test_pack_unpack(S, rows, cols, dt):
+    t = DT[dt]
+    for pad, lead in ((0, 0), (5, 3)):
+        x = Guarded(rows, cols, t, pad, lead, spread(rows, cols, rows + cols))
+        a = S.act_alloc(rows, cols, DEV)
+        a.codes.fill_(99)
+        a.scales.fill_(99)
+        S.act_pack(x.t, a)
+        q, s = codes_of(a)
+        wq, ws = A.pack(f32(x.t))
+        assert np.array_equal(q, wq) and np.array_equal(s, ws)
+        out = Guarded(rows, cols, t, pad, lead)
+        S.act_unpack(a, out.t)
+        want = A.unpack(wq, ws, cols)
+        assert np.array_equal(f32(out.t), want.astype(np.float32))  # exact in every type it was packed from
+        out.check()
+        gain = torch.from_numpy(np.random.default_rng(1).standard_normal(cols).astype(np.float32)).to(DEV)
+        S.act_unpack(a, out.t, gain=gain)
+        prod = f32(torch.from_numpy(want.astype(np.float32) * gain.cpu().numpy()).to(t))  # one fp32 product, rounded
+        assert np.array_equal(f32(out.t), prod)
+        out.check()
+
+
+def test_pack_special_values(S):
+    x = np.zeros((12, 96), dtype=np.float32)
+    x[0, 5], x[1, 40], x[2, 95] = np.inf, -np.inf, np.nan
+    x[0, 6:30] = 3.0
+    x[3] = np.float32(2.0 ** -149)
+    x[4, ::2] = np.finfo(np.float32).max
+    x[5, :32] = np.arange(32) * 0.5 + 111.5  # ties at quantum 1
+    x[6, :32] = -(np.arange(32) * 0.5 + 111.5)
+    x[7, 0] = np.nextafter(np.float32(127.0), np.float32(0))
+    x[8, 0] = np.nextafter(np.float32(127.0), np.float32(200))
+    x[9, :4] = 127.0, 126.5, 125.5, -0.5
+    x[10, 0], x[10, 1] = 2.0 ** -120, 2.0 ** -140
+    x[11] = -0.0
+    xt = torch.from_numpy(x).to(DEV)
+    a = S.act_alloc(12, 96, DEV)
+    S.act_pack(xt, a)
+    q, s = codes_of(a)
+    wq, ws = A.pack(x)
+    assert np.array_equal(q, wq) and np.array_equal(s, ws)
+    out = torch.empty(12, 96, device=DEV)
+    S.act_unpack(a, out)
+    assert np.array_equal(f32(out), A.unpack(wq, ws, 96).astype(np.float32), equal_nan=True)
+    # the largest numbers of each type come back finite
+    for t in DT.values():
+        m = torch.full((2, 64), torch.finfo(t).max, dtype=t, device=DEV)
+        m[1] = -m[1]
+        a, o = S.act_alloc(2, 64, DEV), torch.empty_like(m)
+        S.act_pack(m, a)
+        S.act_unpack(a, o)
+        assert torch.isfinite(o).all() and (o.float() / m.float() - 1).abs().max() < 0.03
+
+
+def test_pack_many_rows_and_far_offsets(S):
+    # the walk of a capped grid, and rows further apart than 2^32 bytes
+    rows, cols = 70000, 96
+    x = torch.randn(rows, cols, device=DEV, dtype=torch.bfloat16, generator=torch.Generator(DEV).manual_seed(1))
+    a = S.act_alloc(rows, cols, DEV)
+    S.act_pack(x, a)
+    wq, ws = A.pack(f32(x))
+    q, s = codes_of(a)
+    assert np.array_equal(q, wq) and np.array_equal(s, ws)
+    ld = (1 << 30) + 1
+    far = torch.empty(4 * ld, dtype=torch.bfloat16, device=DEV)[:].view(4, ld)[:, :100]
+    far.copy_(torch.from_numpy(spread(4, 100, 9)))
+    b = S.act_alloc(4, 100, DEV)
+    S.act_pack(far, b)
+    wq, ws = A.pack(f32(far))
+    q, s = codes_of(b)
+    assert np.array_equal(q, wq) and np.array_equal(s, ws)
+    far.zero_()
+    S.act_unpack(b, far)
+    assert np.array_equal(f32(far), A.unpack(wq, ws, 100).astype(np.float32))
+
+
+# ---------------------------------------------------------------- RMS norm
+
+NORM_SHAPES = [(1, 1), (3, 31), (5, 33), (1, 2048), (9, 777), (67, 1280), (6, 4096), (5, 4097), (3, 5632), (2, 16384),
+               (2, 16421), (2300, 520)]
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("rows,cols", NORM_SHAPES)
+def test_rmsnorm_forward(S, rows, cols, dt):
+    t = DT[dt]
+    for res, pad, lead in ((True, 0, 0), (False, 3, 1), (True, 9, 2)):
+        x = Guarded(rows, cols, t, pad, lead, spread(rows, cols, rows * cols))
+        r = Guarded(rows, cols, t, pad, 0, spread(rows, cols, 7, 0.3)) if res else None
+        w = torch.from_numpy(np.random.default_rng(2).standard_normal(cols).astype(np.float32)).to(DEV)
+        y, h = Guarded(rows, cols, t, pad, lead), Guarded(rows, cols, t, 0, lead)
+        a, rstd = S.act_alloc(rows, cols, DEV), torch.empty(rows, device=DEV)
+        S.rmsnorm_pack(x.t, w, EPS, y.t, xhat=a, rstd=rstd, residual=r.t if res else None, h=h.t)
+        hs = A.norm_sum(f32(x.t), f32(r.t) if res else None)
+        assert torch.equal(h.t.cpu(), torch.from_numpy(hs).to(t))
+        want_r = A.norm_rstd(hs, EPS)
+        rs = rstd.cpu().numpy()
+        # one rounding to fp32 of a binary64 value (a few of whose own last bits are open)
+        assert (np.abs(rs - want_r) <= want_r * U * (1 + 1e-6)).all()
+        xh = hs * rs[:, None]
+        q, s = codes_of(a)
+        wq, ws = A.pack(xh)
+        assert np.array_equal(q, wq) and np.array_equal(s, ws)
+        want, _ = A.norm_forward(f32(x.t), w.cpu().numpy(), EPS, f32(r.t) if res else None)
+        # rstd, hs * rstd and the product with the weight round once each
+        tol = np.abs(want) * (3 * U * (1 + 1e-5) + HALF[t] * (1 + 4 * U)) + 2 * LEAST[t]
+        within(y.t, want, tol, "y")
+        y.check()
+        h.check()
+
+
+@pytest.mark.parametrize("cols", [520, 5000, 17000])
+def test_rmsnorm_optional_outputs_and_places(S, cols):
+    rows = 5
+    g = torch.Generator(DEV).manual_seed(3)
+    x, r = (torch.randn(rows, cols, device=DEV, dtype=torch.bfloat16, generator=g) for _ in range(2))
+    w = torch.randn(cols, device=DEV, generator=g)
+    y, h = torch.empty_like(x), torch.empty_like(x)
+    a, rstd = S.act_alloc(rows, cols, DEV), torch.empty(rows, device=DEV)
+    S.rmsnorm_pack(x, w, EPS, y, xhat=a, rstd=rstd, residual=r, h=h)
+    y2 = torch.empty_like(x)
+    S.rmsnorm_pack(x, w, EPS, y2, residual=r)
+    assert torch.equal(y, y2)
+    b = S.act_alloc(rows, cols, DEV)
+    S.rmsnorm_pack(x, None, EPS, xhat=b, residual=r)
+    assert torch.equal(a.codes, b.codes) and torch.equal(a.scales, b.scales)
+    # h in residual's place, y in x's
+    x2, r2 = x.clone(), r.clone()
+    S.rmsnorm_pack(x2, w, EPS, x2, xhat=b, residual=r2, h=r2)
+    assert torch.equal(x2, y) and torch.equal(r2, h)
+    assert torch.equal(a.codes, b.codes)
+    # one operand in both places
+    y3, h3 = torch.empty_like(x), torch.empty_like(x)
+    S.rmsnorm_pack(x, w, EPS, y3, residual=x, h=h3)
+    assert torch.equal(h3, (x.float() * 2).to(torch.bfloat16))
+
+
+def test_rmsnorm_special_rows(S):
+    x = torch.zeros(5, 96, device=DEV)
+    x[1, 3] = float("inf")
+    x[2, 40] = float("nan")
+    x[3] = 3e38
+    x[4] = 1e-30
+    w = torch.ones(96, device=DEV)
+    y, a, rstd = torch.empty_like(x), S.act_alloc(5, 96, DEV), torch.empty(5, device=DEV)
+    S.rmsnorm_pack(x, w, EPS, y, xhat=a, rstd=rstd)
+    r = rstd.cpu().numpy()
+    s = a.scales.cpu().numpy()
+    assert r[0] == np.float32(1 / np.sqrt(np.float64(np.float32(EPS)))) and (y[0] == 0).all() and not s[0].any()
+    assert r[1] == 0.0 and torch.isnan(y[1, 3]) and s[1].tolist() == [255, 0, 0]  # inf * 0
+    assert np.isnan(r[2]) and torch.isnan(y[2]).all() and s[2].tolist() == [255, 255, 255]
+    assert torch.allclose(y[3], torch.ones_like(y[3]), atol=1e-6)  # the squares pass the range of fp32
+    assert torch.isfinite(y[4]).all()
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("rows,cols", NORM_SHAPES)
+def test_rmsnorm_backward(S, rows, cols, dt):
+    t = DT[dt]
+    r = np.random.default_rng(rows + cols)
+    xh = r.standard_normal((rows, cols)).astype(np.float32)
+    xh[r.random(rows) < 0.1] = 0.0
+    q, s = A.pack(xh)
+    a, x8 = fill_act(S, q, s, cols), A.unpack(q, s, cols)
+    rs = np.exp(r.standard_normal(rows)).astype(np.float32)
+    w = r.standard_normal(cols).astype(np.float32)
+    rstd, wt = torch.from_numpy(rs).to(DEV), torch.from_numpy(w).to(DEV)
+    ws = torch.empty(S.rmsnorm_workspace_bytes(rows, cols), dtype=torch.uint8, device=DEV)
+    for res, pad, lead, acc in ((True, 0, 0, False), (False, 3, 1, True)):
+        dy = Guarded(rows, cols, t, pad, lead, spread(rows, cols, 11))
+        dres = Guarded(rows, cols, t, pad, 0, spread(rows, cols, 12)) if res else None
+        dh = Guarded(rows, cols, t, pad, lead)
+        old = r.standard_normal(cols).astype(np.float32)
+        flat = Guarded(1, cols, torch.float32, 0, 5, old[None])
+        S.rmsnorm_backward(dy.t, a, rstd, wt, dh.t, flat.t.view(-1), ws, dres=dres.t if res else None, accumulate=acc)
+        dyn, dr = f32(dy.t).astype(np.float64), f32(dres.t).astype(np.float64) if res else None
+        want, dw = A.norm_backward(dyn, x8, rs, w, dr)
+        gv = np.abs(dyn * w)
+        mean_abs = (gv * np.abs(x8)).mean(axis=1, keepdims=True)
+        depth = cols / 64 + 24  # longest chain of a row's sum: a lane's columns, the tree, the quotient
+        rest = 0.0 if dr is None else np.abs(dr)
+        mag = rs[:, None].astype(np.float64) * (gv + np.abs(x8) * mean_abs) + rest
+        tol = U * (rs[:, None] * (5 * gv + np.abs(x8) * mean_abs * (depth + 5)) + 2 * rest) * 1.01
+        tol = tol + HALF[t] * np.minimum(np.abs(want) + tol, mag * 1.01) + 2 * LEAST[t]
+        within(dh.t, want, tol, "dh")
+        dh.check()
+        base = old.astype(np.float64) if acc else 0.0
+        # products are fused into the sum: a chain of at most rows + 16 roundings
+        within(flat.t.view(-1), dw + base, U * ((rows + 16) * (np.abs(dyn) * np.abs(x8)).sum(axis=0) +
+                                                2 * np.abs(dw + base)) * 1.01 + 1e-45, "dweight")
+        flat.check()
+
+
+@pytest.mark.parametrize("cols", [520, 5000, 17000])
+def test_rmsnorm_backward_places(S, cols):
+    rows = 300
+    g = torch.Generator(DEV).manual_seed(4)
+    x, dy, dres = (torch.randn(rows, cols, device=DEV, dtype=torch.bfloat16, generator=g) for _ in range(3))
+    w = torch.randn(cols, device=DEV, generator=g)
+    y, a, rstd = torch.empty_like(x), S.act_alloc(rows, cols, DEV), torch.empty(rows, device=DEV)
+    S.rmsnorm_pack(x, w, EPS, y, xhat=a, rstd=rstd)
+    ws = torch.empty(S.rmsnorm_workspace_bytes(rows, cols), dtype=torch.uint8, device=DEV)
+    dh, dw = torch.empty_like(x), torch.empty(cols, device=DEV)
+    S.rmsnorm_backward(dy, a, rstd, w, dh, dw, ws, dres=dres)
+    for place in (0, 1):
+        p = [dy.clone(), dres.clone()]
+        dw2 = torch.empty_like(dw)
+        S.rmsnorm_backward(p[0], a, rstd, w, p[place], dw2, ws, dres=p[1])
+        assert torch.equal(p[place], dh) and torch.equal(dw2, dw)
+    dh3, dw3 = torch.empty_like(dh), torch.empty_like(dw)
+    S.rmsnorm_backward(dy, a, rstd, w, dh3, None, ws, dres=dres)
+    S.rmsnorm_backward(dy, a, rstd, w, None, dw3, ws)
+    assert torch.equal(dh3, dh) and torch.equal(dw3, dw)
+    one = torch.empty_like(dy)
+    S.rmsnorm_backward(dy, a, rstd, w, one, dw3, ws, dres=dy)  # one tensor as both gradients
+    within(one, f32(one).astype(np.float64), 0.0, "finite")
+
+
+# ----------------------------------------------------------- weight gradient
+
+WGRAD_SHAPES = [(1, 1, 1), (1, 64, 64), (7, 33, 5), (31, 32, 130), (64, 777, 129), (257, 129, 257), (33, 520, 1531),
+                (1000, 256, 256), (4099, 130, 64), (700, 1, 3), (700, 3, 1)]
+
+
+def exact_inputs(rows, n_in, n_out, dt, seed):
+    """Integers whose products and sums are exact in fp32 in any order, and
+    that need every significant bit of dy's type."""
+    r = np.random.default_rng(seed)
+    q = r.integers(-127, 128, (rows, A.BLOCK * -(-n_in // A.BLOCK))).astype(np.int8)
+    q[:, n_in:] = 0
+    s = r.choice(np.array([126, 127, 128, 0], dtype=np.uint8), (rows, q.shape[1] // A.BLOCK), p=[0.3, 0.3, 0.3, 0.1])
+    q[np.repeat(s == 0, A.BLOCK, axis=1)] = 0
+    # |sum| < 2^24 half units: the room that rows of 254 leave for dy
+    room = int(2 ** 24 // (2 * 254 * max(rows, 1)))
+    top = {"bf16": 255, "fp16": 2047, "fp32": 1 << 22}[dt]
+    top = max(1, min(top, room))
+    dy = r.integers(-top, top + 1, (rows, n_out)).astype(np.float64)
+    return q, s, dy
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("rows,n_in,n_out", WGRAD_SHAPES)
+def test_wgrad_exact(S, rows, n_in, n_out, dt):
+    q, s, dyn = exact_inputs(rows, n_in, n_out, dt, rows + n_in + n_out)
+    a = fill_act(S, q, s, n_in)
+    want, wb = A.wgrad(dyn, A.unpack(q, s, n_in))
+    ws = torch.empty(S.wgrad_workspace_bytes(rows, n_in, n_out), dtype=torch.uint8, device=DEV)
+    for pad, lead in ((0, 0), (3, 1)):
+        dy = Guarded(rows, n_out, DT[dt], pad, lead, dyn)
+        dw = Guarded(1, n_out * n_in, torch.float32, 0, 3)
+        db = Guarded(1, n_out, torch.float32, 0, 1)
+        S.wgrad(dy.t, a, dw.t.view(-1), ws, dbias=db.t.view(-1))
+        assert np.array_equal(f32(dw.t).reshape(n_out, n_in), want.astype(np.float32))
+        assert np.array_equal(f32(db.t)[0], wb.astype(np.float32))
+        S.wgrad(dy.t, a, dw.t.view(-1), ws, dbias=db.t.view(-1), accumulate=True)
+        assert np.array_equal(f32(dw.t).reshape(n_out, n_in), 2 * want.astype(np.float32))
+        assert np.array_equal(f32(db.t)[0], 2 * wb.astype(np.float32))
+        dw.check()
+        db.check()
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("rows,n_in,n_out", [(5, 100, 70), (300, 260, 130), (5000, 136, 200)])
+def test_wgrad_values(S, rows, n_in, n_out, dt):
+    t = DT[dt]
+    r = np.random.default_rng(rows)
+    x = spread(rows, n_in, 21).astype(np.float32)
+    q, s = A.pack(x)
+    a, x8 = fill_act(S, q, s, n_in), A.unpack(q, s, n_in)
+    gain = r.standard_normal(n_in).astype(np.float32)
+    dy = Guarded(rows, n_out, t, 0, 0, spread(rows, n_out, 22))
+    dyn = f32(dy.t).astype(np.float64)
+    want, wb = A.wgrad(dyn, x8, gain)
+    size = np.abs(dyn).T @ np.abs(x8) * np.abs(gain)
+    ws = torch.empty(S.wgrad_workspace_bytes(rows, n_in, n_out), dtype=torch.uint8, device=DEV)
+    dw, db = torch.empty(n_out, n_in, device=DEV), torch.empty(n_out, device=DEV)
+    S.wgrad(dy.t, a, dw, ws, gain=torch.from_numpy(gain).to(DEV), dbias=db)
+    # exact products, rows * terms of them, each sum off by at most a unit in the last place; then the gain
+    terms = {"bf16": 1, "fp16": 2, "fp32": 3}[dt]
+    within(dw, want, 2 * U * (rows * terms + 8) * size, "dw")
+    within(db, wb, U * (rows + 8) * np.abs(dyn).sum(axis=0), "dbias")
+    # the errors of a sum add up like a random walk
+    rel = np.linalg.norm(f32(dw) - want) / np.linalg.norm(want)
+    assert rel < 2 * U * np.sqrt(rows * terms + 8) * np.linalg.norm(size) / np.linalg.norm(want)
+    dw2 = torch.empty_like(dw)
+    S.wgrad(dy.t, a, dw2, ws, gain=torch.from_numpy(gain).to(DEV))
+    assert torch.equal(dw, dw2)
+
+
+def test_wgrad_nonfinite(S):
+    q, s, dyn = exact_inputs(64, 64, 40, "bf16", 5)
+    for dt in DT:
+        sc = s.copy()
+        sc[3, 1], q2 = 255, q.copy()
+        q2[3, 32:] = 0
+        a = fill_act(S, q2, sc, 64)
+        dy = torch.from_numpy(dyn).to(DEV, DT[dt])
+        dy[7, 5] = float("nan")
+        ws = torch.empty(S.wgrad_workspace_bytes(64, 64, 40), dtype=torch.uint8, device=DEV)
+        dw, db = torch.empty(40, 64, device=DEV), torch.empty(40, device=DEV)
+        S.wgrad(dy, a, dw, ws, dbias=db)
+        nan = torch.isnan(dw).cpu().numpy()
+        assert nan[:, 32:].all() and nan[5].all() and not nan[:5, :32].any() and not nan[6:, :32].any()
+        assert torch.isnan(db).nonzero().flatten().tolist() == [5]
+        dy[7, 5] = float("inf")
+        S.wgrad(dy, fill_act(S, np.ones_like(q), np.full_like(s, 127), 64), dw, ws, dbias=db)
+        assert torch.isinf(dw[5]).all() and torch.isfinite(dw[:5]).all() and torch.isfinite(dw[6:]).all()
+
+
+def test_no_rows(S):
+    a = S.act_alloc(0, 40, DEV)
+    x = torch.empty(0, 40, device=DEV)
+    S.act_pack(x, a)
+    S.act_unpack(a, x)
+    w = torch.ones(40, device=DEV)
+    rstd = torch.empty(0, device=DEV)
+    S.rmsnorm_pack(x, w, EPS, x, xhat=a, rstd=rstd)
+    ws = torch.empty(S.rmsnorm_workspace_bytes(0, 40), dtype=torch.uint8, device=DEV)
+    dw = torch.ones(40, device=DEV)
+    S.rmsnorm_backward(x, a, rstd, w, x, dw, ws, accumulate=True)
+    assert (dw == 1).all()
+    S.rmsnorm_backward(x, a, rstd, w, x, dw, ws)
+    assert (dw == 0).all()
+    ws = torch.empty(S.wgrad_workspace_bytes(0, 40, 8), dtype=torch.uint8, device=DEV)
+    dy, dw, db = torch.empty(0, 8, device=DEV), torch.ones(8, 40, device=DEV), torch.ones(8, device=DEV)
+    S.wgrad(dy, a, dw, ws, dbias=db, accumulate=True)
+    assert (dw == 1).all() and (db == 1).all()
+    S.wgrad(dy, a, dw, ws, dbias=db)
+    assert (dw == 0).all() and (db == 0).all()
+
+
+def test_binding_refuses(S):
+    x = torch.zeros(4, 64, device=DEV)
+    a, w, rstd = S.act_alloc(4, 64, DEV), torch.ones(64, device=DEV), torch.empty(4, device=DEV)
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+    dw = torch.empty(64, 64, device=DEV)
+    for bad in (lambda: S.act_pack(x[0], a), lambda: S.act_pack(x.double(), a), lambda: S.act_pack(x[:3], a),
+                lambda: S.act_pack(x.t(), S.act_alloc(64, 4, DEV)),
+                lambda: S.act_pack(x[:1].expand(4, 64), a), lambda: S.act_unpack(a, x[:, ::2]),
+                lambda: S.act_unpack(a, x, gain=w[:63]), lambda: S.act_unpack(a, x, gain=w.double()),
+                lambda: S.act_unpack(a, x, gain=torch.ones(64)),
+                lambda: S.rmsnorm_pack(x, w, EPS, x[:2]), lambda: S.rmsnorm_pack(x, w, EPS, x, rstd=rstd[:3]),
+                lambda: S.rmsnorm_backward(x, a, rstd, w, x, w, ws[:8]),
+                lambda: S.rmsnorm_backward(x, a, rstd, w, x, w, ws[8:]),
+                lambda: S.wgrad(x, a, dw[:, :32], ws), lambda: S.wgrad(x, a, dw.half(), ws),
+                lambda: S.wgrad(x, a, None, ws), lambda: S.wgrad(x[:3], a, dw, ws),
+                lambda: S.wgrad(x, a, dw, ws.cpu()),
+                lambda: S.ActCheckpoint(a.codes[:, :32], a.scales, 64),
+                lambda: S.act_in(ws[1:], 4, 64)):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: S.act_pack(x, None), lambda: S.rmsnorm_pack(x, w, EPS), lambda: S.rmsnorm_pack(x, w, 0.0, x),
+                lambda: S.rmsnorm_pack(x, None, EPS, x), lambda: S.rmsnorm_pack(x, w, EPS, x, h=x),
+                lambda: S.rmsnorm_pack(x, w, EPS, x.half()),
+                lambda: S.rmsnorm_backward(x, a, rstd, w, None, None, ws)):
+        with pytest.raises(S.ScapeError):
+            bad()
+
+
+# --------------------------------------------- streams, graphs, a whole run
+
+
+def layer_pass(S, st):
+    """Norm of a residual stream, two linear layers behind it, backward."""
+    S.rmsnorm_pack(st["x"], st["w"], EPS, st["y"], xhat=st["xh"], rstd=st["rstd"], residual=st["res"], h=st["h"])
+    S.wgrad(st["dout"], st["xh"], st["row"][st["off_w"]:st["off_w"] + st["dout"].shape[1] * st["x"].shape[1]],
+            st["ws"], gain=st["w"], dbias=st["row"][st["off_b"]:st["off_b"] + st["dout"].shape[1]])
+    S.rmsnorm_backward(st["dy"], st["xh"], st["rstd"], st["w"], st["dh"],
+                       st["row"][st["off_n"]:st["off_n"] + st["x"].shape[1]], st["nws"], dres=st["dres"])
+
+
+def layer_state(S, rows, cols, n_out, dtype, seed):
+    g = torch.Generator(DEV).manual_seed(seed)
+    rnd = lambda *sh: torch.randn(*sh, device=DEV, generator=g)  # noqa: E731
+    st = {k: rnd(rows, cols).to(dtype) for k in ("x", "res", "dy", "dres")}
+    st["w"], st["dout"] = 1 + 0.2 * rnd(cols), rnd(rows, n_out).to(dtype)
+    st["y"], st["h"], st["dh"] = (torch.zeros(rows, cols, dtype=dtype, device=DEV) for _ in range(3))
+    st["xh"], st["rstd"] = S.act_alloc(rows, cols, DEV), torch.zeros(rows, device=DEV)
+    # one worker's gradient row: norm weight, then the layer's weight and bias, at odd offsets
+    st["off_n"], st["off_w"] = 1, cols + 2
+    st["off_b"] = st["off_w"] + n_out * cols
+    st["row"] = torch.zeros(st["off_b"] + n_out + 3, device=DEV)
+    st["ws"] = torch.empty(S.wgrad_workspace_bytes(rows, cols, n_out), dtype=torch.uint8, device=DEV)
+    st["nws"] = torch.empty(S.rmsnorm_workspace_bytes(rows, cols), dtype=torch.uint8, device=DEV)
+    return st
+
+
+OUT = ("y", "h", "dh", "row", "rstd")
+
+
+@pytest.mark.parametrize("rows,cols,n_out,dtype", [(37, 96, 40, torch.float32), (700, 200, 130, torch.bfloat16)])
+def test_layer_pass_against_oracle(S, rows, cols, n_out, dtype):
+    st = layer_state(S, rows, cols, n_out, dtype, 8)
+    layer_pass(S, st)
+    q, s = codes_of(st["xh"])
+    x8, w = A.unpack(q, s, cols), f32(st["w"])
+    dh, dwn = A.norm_backward(f32(st["dy"]), x8, f32(st["rstd"]), w, f32(st["dres"]))
+    dw, db = A.wgrad(f32(st["dout"]), x8, w)
+    row = f32(st["row"]).astype(np.float64)
+    cut = lambda k, n: row[st[k]:st[k] + n]  # noqa: E731
+    size = np.abs(f32(st["dout"]).astype(np.float64)).T @ np.abs(x8) * np.abs(w)
+    within(cut("off_w", n_out * cols).reshape(n_out, cols), dw, 2 * U * (3 * rows + 8) * size, "dw")
+    within(cut("off_b", n_out), db, U * (rows + 8) * np.abs(f32(st["dout"])).sum(axis=0), "db")
+    within(cut("off_n", cols), dwn, U * (rows + 16) * np.abs(f32(st["dy"]) * x8).sum(axis=0) * 1.01, "dweight")
+    assert np.linalg.norm(f32(st["dh"]) - dh) <= (HALF[dtype] + 64 * U) * np.linalg.norm(dh) * 2
+    assert row[0] == 0 and row[cols + 1] == 0 and not row[-3:].any()
+
+
+def test_other_stream_and_repeat(S):
+    st = layer_state(S, 700, 200, 130, torch.bfloat16, 9)
+    layer_pass(S, st)
+    torch.cuda.synchronize()
+    want = {k: st[k].clone() for k in OUT}
+    for k in OUT:
+        st[k].zero_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer_pass(S, st)
+    side.synchronize()
+    for k in OUT:
+        assert torch.equal(st[k], want[k]), k
+    # an explicit stream argument
+    y2 = torch.zeros_like(st["y"])
+    torch.cuda.synchronize()
+    S.rmsnorm_pack(st["x"], st["w"], EPS, y2, residual=st["res"], stream=side)
+    side.synchronize()
+    assert torch.equal(y2, want["y"])
+
+
+def test_two_streams_at_once(S):
+    sts = [layer_state(S, 1500, 264, 200, torch.bfloat16, 20 + i) for i in range(2)]
+    for st in sts:
+        layer_pass(S, st)
+    torch.cuda.synchronize()
+    want = [{k: st[k].clone() for k in OUT} for st in sts]
+    streams = [torch.cuda.Stream() for _ in sts]
+    for _ in range(5):
+        for st, side in zip(sts, streams):
+            with torch.cuda.stream(side):
+                for k in OUT:
+                    st[k].zero_()
+                layer_pass(S, st)
+    torch.cuda.synchronize()
+    for st, w in zip(sts, want):
+        for k in OUT:
+            assert torch.equal(st[k], w[k]), k
+
+
+def test_captured_and_replayed(S):
+    st = layer_state(S, 700, 200, 130, torch.bfloat16, 10)
+    layer_pass(S, st)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer_pass(S, st)
+    for i in range(4):
+        g = torch.Generator(DEV).manual_seed(50 + i)
+        for k in ("x", "res", "dy", "dres", "dout"):
+            st[k].copy_(torch.randn(st[k].shape, device=DEV, generator=g))
+        for k in OUT:
+            st[k].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {k: st[k].clone() for k in OUT}
+        for k in OUT:
+            st[k].zero_()
+        layer_pass(S, st)
+        torch.cuda.synchronize()
+        for k in OUT:
+            assert torch.equal(got[k], st[k]), (i, k)
+
+
+def test_gradient_rows_into_the_optimizer_step(S):
+    """Two workers' backward passes write a one-layer model's gradient rows;
+    the optimizer step on them equals the step oracle on the same rows."""
+    from oracle import scape_oracle as O
+    rows, cols, n_out, K, P = 96, 64, 46, 2, 2
+    n = cols + n_out * cols + n_out  # norm weight, layer weight, bias
+    assert n % P == 0
+    r = np.random.default_rng(31)
+    w0 = (r.standard_normal(n) * 0.02).astype(np.float32)
+    w0[:cols] = 1.0
+    k = n // P // 10
+    opt = S.ScapeOptimizer(torch.from_numpy(w0).to(DEV), P, K, k)
+    ora = O.OracleOptimizer(w0, P, K, k, O.Hyper.make(0.9, 0.95, 1e-8, 0.0, 1e-3))
+    grads = torch.zeros(K, n, device=DEV)
+    ws = torch.empty(S.wgrad_workspace_bytes(rows, cols, n_out), dtype=torch.uint8, device=DEV)
+    nws = torch.empty(S.rmsnorm_workspace_bytes(rows, cols), dtype=torch.uint8, device=DEV)
+    xh, rstd = S.act_alloc(rows, cols, DEV), torch.empty(rows, device=DEV)
+    y, dh = (torch.empty(rows, cols, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    for t in range(1, 4):
+        for i in range(K):
+            for micro in range(2):  # two micro-batches add up in the row
+                g = torch.Generator(DEV).manual_seed(1000 * t + 10 * i + micro)
+                x = torch.randn(rows, cols, device=DEV, generator=g).to(torch.bfloat16)
+                target = torch.randn(rows, n_out, device=DEV, generator=g)
+                gamma = opt.params[:cols]
+                weight = opt.params[cols:cols + n_out * cols].view(n_out, cols)
+                bias = opt.params[cols + n_out * cols:]
+                S.rmsnorm_pack(x, gamma, EPS, y, xhat=xh, rstd=rstd)
+                dout = (y.float() @ weight.t() + bias - target).to(torch.bfloat16)
+                dy = (dout.float() @ weight).to(torch.bfloat16)
+                row = grads[i]
+                S.wgrad(dout, xh, row[cols:cols + n_out * cols], ws, gain=gamma, dbias=row[cols + n_out * cols:],
+                        accumulate=micro > 0)
+                S.rmsnorm_backward(dy, xh, rstd, gamma, dh, row[:cols], nws, accumulate=micro > 0)
+        host = grads.cpu().numpy()
+        assert np.isfinite(host).all() and (host != 0).mean() > 0.9
+        opt.step(grads)
+        ora.step(host)
+    torch.cuda.synchronize()
+    for name, want in (("params", ora.gather("w")), ("m", ora.gather("m")), ("e", ora.gather("e"))):
+        assert np.array_equal(getattr(opt, name).cpu().numpy().view(np.uint32), want.view(np.uint32)), name
