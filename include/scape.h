@@ -506,9 +506,11 @@ scape_status scape_rmsnorm_backward(int64_t rows, int64_t cols, scape_matrix dy,
                                     float* dweight, int32_t accumulate, void* workspace, size_t workspace_bytes,
                                     hipStream_t stream);
 
-/* Bytes of scratch scape_wgrad needs (256-byte aligned).  0 if a size is
- * invalid. */
-size_t scape_wgrad_workspace_bytes(int64_t rows, int64_t in, int64_t out);
+/* Bytes of scratch scape_wgrad needs with this dy (256-byte aligned): the
+ * checkpoint as bf16, dy's bf16 terms (none for a bf16 dy of 16-byte aligned
+ * rows with out % 8 == 0) and partial sums.  dy.data null: enough for any dy.
+ * 0 if a size is invalid. */
+size_t scape_wgrad_workspace_bytes(int64_t rows, int64_t in, int64_t out, scape_matrix dy);
 
 /*
  * Gradient of a linear layer's weight [out][in] and bias [out] from the

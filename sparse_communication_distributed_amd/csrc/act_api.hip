@@ -143,9 +143,9 @@ scape_status scape_rmsnorm_backward(int64_t rows, int64_t cols, scape_matrix dy,
                    "rmsnorm backward");
 }
 
-size_t scape_wgrad_workspace_bytes(int64_t rows, int64_t in, int64_t out) {
+size_t scape_wgrad_workspace_bytes(int64_t rows, int64_t in, int64_t out, scape_matrix dy) {
   if (!rows_ok(rows) || !cols_ok(in) || !cols_ok(out) || in * out > kMaxWeight) return 0;
-  return align256(wgrad_workspace(rows, in, out));
+  return wgrad_workspace(rows, in, out, dy);
 }
 
 scape_status scape_wgrad(int64_t rows, int64_t in, int64_t out, scape_matrix dy, scape_act_view x, const float* gain,
@@ -161,12 +161,11 @@ scape_status scape_wgrad(int64_t rows, int64_t in, int64_t out, scape_matrix dy,
   if (!dw) return fail(SCAPE_EINVAL, "dw is null");
   if (misaligned4(gain) || misaligned4(dw) || misaligned4(dbias))
     return fail(SCAPE_EINVAL, "gain, dw and dbias must be 4-byte aligned");
-  const size_t need = scape_wgrad_workspace_bytes(rows, in, out);
+  const size_t need = wgrad_workspace(rows, in, out, dy);
   if (!workspace) return fail(SCAPE_EINVAL, "workspace is null");
   if (workspace_bytes < need)
     return fail(SCAPE_EWORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
-  return hip_check(launch_wgrad(rows, in, out, dy, x, gain, dw, dbias, accumulate != 0,
-                                static_cast<float*>(workspace), stream),
+  return hip_check(launch_wgrad(rows, in, out, dy, x, gain, dw, dbias, accumulate != 0, workspace, stream),
                    "wgrad");
 }
 

@@ -27,12 +27,11 @@ hipError_t launch_rmsnorm_backward(int64_t rows, int64_t cols, const scape_matri
                                    const float* rstd, const float* weight, const scape_matrix& dres,
                                    const scape_matrix& dh, float* dweight, bool accumulate, float* parts,
                                    hipStream_t s);
-// Splits of the rows of a weight gradient (1: none), each with a partial sum
-// [out][in] (and [out] of the bias) in the workspace.
-int wgrad_splits(int64_t rows, int64_t in, int64_t out);
-size_t wgrad_workspace(int64_t rows, int64_t in, int64_t out);
+// Bytes of scratch of a weight gradient: the checkpoint as bf16, dy's terms
+// (those of every type's dy where dy.data is null), the splits' partial sums.
+size_t wgrad_workspace(int64_t rows, int64_t in, int64_t out, const scape_matrix& dy);
 hipError_t launch_wgrad(int64_t rows, int64_t in, int64_t out, const scape_matrix& dy, const scape_act_view& x,
-                        const float* gain, float* dw, float* dbias, bool accumulate, float* ws, hipStream_t s);
+                        const float* gain, float* dw, float* dbias, bool accumulate, void* ws, hipStream_t s);
 
 #ifdef __HIPCC__
 

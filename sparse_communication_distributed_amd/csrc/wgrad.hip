@@ -4,6 +4,10 @@
 // a power of two as their scale, so they are exact in bf16; a bf16 dy is
 // taken as it is, and fp16 and fp32 are split into 2 and 3 bf16 terms that
 // add up to the value.  So every product is exact and only the sums round.
+//
+// Launches: prepare (the checkpoint as bf16, and dy's terms where dy cannot
+// be read as it lies), the product over row splits, and with more than one
+// split the join of their partial sums.
 
 #include "activations.h"
 
@@ -12,28 +16,30 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) char lds_char;
 
-constexpr int kBM = 128;         // out per workgroup
-constexpr int kBN = 128;         // in per workgroup
-constexpr int kBK = 32;          // rows per stage
-constexpr int kLdsK = kBK + 8;   // padded k extent of a staged column
-constexpr int kMinSplitRows = 128;
-constexpr int kTargetBlocks = 512;
-
+constexpr int kBK = 32;     // rows a stage
+constexpr int kWaves = 4;
 constexpr int terms_of(int dt) { return dt == SCAPE_F32 ? 3 : dt == SCAPE_F16 ? 2 : 1; }
 
-struct WgradArgs {
-  int64_t rows, in, out, nblk;
-  const void* dy;
-  int64_t dy_ld;
+int64_t ceil_div(int64_t x, int64_t t) { return (x + t - 1) / t; }
+
+// ------------------------------------------------------------------ prepare
+
+struct PrepArgs {
+  int64_t rows, rows_pad, nblk, out, out_pad;
   const int8_t* codes;
   const uint8_t* scales;
-  const float* gain;   // applied here only when there is one split
-  float* dw;           // [splits][out][in], or dw itself (one split)
-  float* db;           // [splits][out], or dbias itself; null: none
-  bool accumulate;     // one split
-  int64_t split_rows;  // rows a split sums (a multiple of kBK)
-  int tiles_m, tiles_n;
+  uint16_t* x;  // [rows_pad][nblk * 32] bf16, zero past rows
+  const void* dy;
+  int64_t dy_ld;
+  // dy's terms [terms][t_rows][out_pad] bf16 of rows t_first .., zero past
+  // dy's rows and columns: all rows, or the last, partial stage of a dy that
+  // is read as it lies (none: t_rows = 0)
+  uint16_t* terms;
+  int64_t t_first, t_rows;
+  unsigned x_blocks;
 };
 
 // Splits v into its leading 8 significant bits (the upper half of its
@@ -43,99 +49,297 @@ __device__ __forceinline__ uint32_t cut_term(float& v) {
   const uint32_t u = __float_as_uint(v) & 0xffff0000u;
   const float h = __uint_as_float(u);
   v = __builtin_isinf(v) ? 0.0f : v - h;
-  return u >> 16;
+  return u;
+}
+// The upper halves of two words, a's in the lower half.
+__device__ __forceinline__ uint32_t upper_halves(uint32_t a, uint32_t b) {
+  return __builtin_amdgcn_perm(b, a, 0x07060302u);
 }
 
 template <int DT>
-__global__ void __launch_bounds__(256) wgrad_kernel(WgradArgs a) {
-  constexpr int NT = terms_of(DT);
-  __shared__ __attribute__((aligned(16))) uint16_t lds_a[NT][kBM][kLdsK];
-  __shared__ __attribute__((aligned(16))) uint16_t lds_b[kBN][kLdsK];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int tile = blockIdx.x;
-  const int64_t m0 = (int64_t)(tile / a.tiles_n) * kBM, n0 = (int64_t)(tile % a.tiles_n) * kBN;
-  const int64_t split = blockIdx.y;
-  const int64_t t_begin = split * a.split_rows;
-  const int64_t t_end = t_begin + a.split_rows < a.rows ? t_begin + a.split_rows : a.rows;
-  const bool bias = a.db && n0 == 0;
-
-  f32x16 acc[2][2];
+__global__ void __launch_bounds__(kThreads) wgrad_prepare_kernel(PrepArgs a) {
+  if (blockIdx.x < a.x_blocks) {
+    const int64_t n = a.rows_pad * a.nblk * 4, step = (int64_t)a.x_blocks * kThreads;
+    const int64_t full = a.rows * a.nblk * 4;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
+      u32x4 p = {0, 0, 0, 0};
+      if (i < full) {
+        float v[8];
+        act_decode(reinterpret_cast<const u32x2*>(a.codes)[i], a.scales[i >> 2], v);
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = (f32x16)(0.0f);
-  float bsum[2] = {0.0f, 0.0f};
-
-  // staging: wave w takes rows 8w .. 8w + 7 of a stage, a lane two columns
-  const int64_t mc = m0 + 2 * lane, nc = n0 + 2 * lane;
-  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
-
-  for (int64_t t0 = t_begin; t0 < t_end; t0 += kBK) {
-    float y[8][2];
-    uint32_t xb[2][8];
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const int64_t t = t0 + wave * 8 + r;
-      const bool in_t = t < t_end;
-      y[r][0] = in_t && mc < a.out ? Elem<DT>::get(a.dy, t * a.dy_ld + mc) : 0.0f;
-      y[r][1] = in_t && mc + 1 < a.out ? Elem<DT>::get(a.dy, t * a.dy_ld + mc + 1) : 0.0f;
-      xb[0][r] = xb[1][r] = 0;
-      if (in_t && nc < a.nblk * kActBlock) {
-        const int64_t b = t * a.nblk + nc / kActBlock;
-        const uint16_t q = *reinterpret_cast<const uint16_t*>(a.codes + b * kActBlock + (nc & 31));
-        const float f = __uint_as_float((uint32_t)a.scales[b] << 23);
-        xb[0][r] = __float_as_uint((float)(int8_t)(q & 0xff) * f) >> 16;
-        xb[1][r] = __float_as_uint((float)(int8_t)(q >> 8) * f) >> 16;
+        for (int h = 0; h < 4; ++h) p[h] = upper_halves(__float_as_uint(v[2 * h]), __float_as_uint(v[2 * h + 1]));
       }
+      reinterpret_cast<u32x4*>(a.x)[i] = p;
     }
+    return;
+  }
+  const int64_t chunks = a.out_pad / 8, n = a.t_rows * chunks;
+  const int64_t step = (int64_t)(gridDim.x - a.x_blocks) * kThreads;
+  for (int64_t i = (int64_t)(blockIdx.x - a.x_blocks) * kThreads + threadIdx.x; i < n; i += step) {
+    const int64_t r = i / chunks, c = (i - r * chunks) * 8, t = a.t_first + r;
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (t < a.rows) load8<DT>(a.dy, t * a.dy_ld, c, a.out, v);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int k = 0; k < terms_of(DT); ++k) {
       u32x4 p;
 #pragma unroll
-      for (int h = 0; h < 4; ++h) p[h] = xb[c][2 * h] | (xb[c][2 * h + 1] << 16);
-      *reinterpret_cast<u32x4*>(&lds_b[2 * lane + c][wave * 8]) = p;
-      if (bias)
+      for (int h = 0; h < 4; ++h) {
+        const uint32_t lo = cut_term(v[2 * h]), hi = cut_term(v[2 * h + 1]);
+        p[h] = upper_halves(lo, hi);
+      }
+      *reinterpret_cast<u32x4*>(a.terms + (k * a.t_rows + r) * a.out_pad + c) = p;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ product
+
+struct WgradArgs {
+  int64_t rows, in, out;
+  const char* a;         // dy or its terms: bf16 rows a_step bytes apart
+  int64_t a_step;
+  int64_t a_plane;       // bytes between terms
+  int64_t a_cols;        // columns that may be read (a multiple of 8)
+  int terms;
+  const char* tail;      // the last, partial stage of a's rows, zero filled; null: none
+  int64_t tail_step;
+  const char* b;         // the checkpoint as bf16, zero past rows to a whole stage
+  int64_t b_step, b_cols;
+  const float* gain;     // applied here only when there is one split
+  float* dw;             // [splits][out][in], or dw itself (one split)
+  float* db;             // [splits][out], or dbias itself; null: none
+  bool accumulate;       // one split
+  int64_t split_rows;    // rows a split sums (a multiple of kBK)
+  int tiles_n, tiles;    // tiles along in, and in all
+};
+
+// A barrier that orders LDS only: loads from memory stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// 16 bytes a lane from memory to LDS without a register: lane l's go to
+// lds + 16 * l.  The address is base (the same for the wave) + off bytes.
+// The compiler does not count it: wait for it with wait_vm.
+__device__ __forceinline__ void load_to_lds(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(lds), "v"(off), "s"(base) : "memory");
+}
+// Waits until at most N of the wave's loads from memory are under way.
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
+// A stage of an operand lies in LDS as in memory, [row][W columns] of bf16.
+// The 4 rows that a transposed read takes have to fall on different banks
+// (256 bytes hold all 64), so the 64-byte pieces of a row are permuted by
+// bits of the row number.
+template <int W>
+__device__ __forceinline__ int piece_at(int piece, int row) {
+  return W == 192 ? piece ^ ((row >> 1) & 1) : piece ^ (row & 3);
+}
+
+// One workgroup sums a BM x BN tile of dw over the rows of one split.  Both
+// operands have the summed index (the rows) as their slow axis and come to
+// LDS as they lie, without a register; the transposed LDS read gives the
+// fragments.  A ring of kRing stages keeps kRing - 2 of them under way.
+template <int BM, int BN, int WM, int WN, int kRing>
+__global__ void __launch_bounds__(kWaves * 64) wgrad_kernel(WgradArgs a) {
+  constexpr int FM = BM / WM / 32, FN = BN / WN / 32;
+  constexpr int kBytesA = BM * kBK * 2, kStage = (BM + BN) * kBK * 2;
+  constexpr int LA = kBytesA / 1024 / kWaves, LB = BN * kBK * 2 / 1024 / kWaves;  // 1 KB loads a wave and stage
+  constexpr int kLoads = LA + LB;
+  static_assert(WM * WN == kWaves && FM * WM * 32 == BM && FN * WN * 32 == BN, "tile shape");
+  static_assert(LA * kWaves * 1024 == kBytesA && LB * kWaves * 1024 == BN * kBK * 2, "whole loads");
+  static_assert(kRing * kStage <= 160 * 1024 && kRing >= 3, "ring");
+  __shared__ __attribute__((aligned(1024))) char lds[kRing * kStage];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // Workgroups are dealt to the 8 XCDs in turn: give each XCD consecutive
+  // tiles, which share dy's columns and the checkpoint's in its L2.
+  const int total = gridDim.x, q8 = total >> 3, r8 = total & 7;
+  const int xcd = blockIdx.x & 7;
+  const int id = xcd * q8 + (xcd < r8 ? xcd : r8) + (blockIdx.x >> 3);
+  const int split = id / a.tiles, tile = id - split * a.tiles;
+  const int64_t m0 = (int64_t)(tile / a.tiles_n) * BM, n0 = (int64_t)(tile % a.tiles_n) * BN;
+  const int64_t t_begin = (int64_t)split * a.split_rows;
+  const int64_t t_end = t_begin + a.split_rows < a.rows ? t_begin + a.split_rows : a.rows;
+  const int stages = t_begin < t_end ? (int)((t_end - t_begin + kBK - 1) / kBK) : 0;  // of one term
+  const int all = stages * a.terms;
+
+  // ---- loads: this lane's place in each 1 KB of this wave.  Columns past
+  // the edge are read from inside the row, multiplied and never stored.
+  uint32_t a_off[LA], t_off[LA], b_off[LB];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) bsum[c] += y[r][c];
+  for (int i = 0; i < LA; ++i) {
+    const int at = (wave * LA + i) * 64 + lane, row = at / (BM / 8), place = at % (BM / 8);
+    int64_t c = m0 + (piece_at<BM>(place >> 2, row) * 4 + (place & 3)) * 8;
+    if (c > a.a_cols - 8) c = a.a_cols - 8;
+    a_off[i] = (uint32_t)(row * a.a_step + c * 2);
+    t_off[i] = (uint32_t)(row * a.tail_step + c * 2);
+  }
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const uint32_t lo = cut_term(y[2 * h][c]), hi = cut_term(y[2 * h + 1][c]);
-          p[h] = lo | (hi << 16);
-        }
-        *reinterpret_cast<u32x4*>(&lds_a[n][2 * lane + c][wave * 8]) = p;
+  for (int i = 0; i < LB; ++i) {
+    const int at = (wave * LB + i) * 64 + lane, row = at / (BN / 8), place = at % (BN / 8);
+    int64_t c = n0 + (piece_at<BN>(place >> 2, row) * 4 + (place & 3)) * 8;
+    if (c > a.b_cols - 8) c = a.b_cols - 8;
+    b_off[i] = (uint32_t)(row * a.b_step + c * 2);
+  }
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char*)lds;
+  const uint32_t lds_a = __builtin_amdgcn_readfirstlane(lds0 + wave * LA * 1024);
+  const uint32_t lds_b = __builtin_amdgcn_readfirstlane(lds0 + kBytesA + wave * LB * 1024);
+
+  // the next stage to load; past the last one it is loaded again, into slots
+  // that nobody reads, so that every stage has the same loads under way
+  const char* a_next = a.a + t_begin * a.a_step;
+  const char* b_next = a.b + t_begin * a.b_step;
+  int next = 0;
+  uint32_t next_at = 0;  // of its slot
+  int left = stages;     // of its term
+  const bool has_tail = a.tail && t_end == a.rows;
+  auto load_a = [&](int i) {
+    const bool t = has_tail && left == 1;
+    load_to_lds(t ? a.tail : a_next, t ? t_off[i] : a_off[i], lds_a + next_at + i * 1024);
+  };
+  auto load_b = [&](int i) { load_to_lds(b_next, b_off[i], lds_b + next_at + i * 1024); };
+  auto advance = [&]() {
+    if (++next < all) {
+      a_next += kBK * a.a_step;
+      b_next += kBK * a.b_step;
+      if (--left == 0) {  // the next term, from the split's first row
+        left = stages;
+        a_next += a.a_plane - stages * (kBK * a.a_step);
+        b_next -= stages * (kBK * a.b_step);
       }
     }
-    __syncthreads();
+    next_at = next_at + kStage == kRing * kStage ? 0 : next_at + kStage;
+  };
+
+  // ---- fragments.  A transposed read takes, in each 16 lanes, 4 rows of 16
+  // columns (lane l: row l/4, columns 4 (l%4) ..) and gives lane l column l.
+  const int wm = wave / WN * (FM * 32), wn = wave % WN * (FN * 32);
+  const int tr = (lane & 15) >> 2;
+  int a_at[FM], b_at[FN];
 #pragma unroll
-    for (int kk = 0; kk < kBK; kk += 16) {
-      const int k = kk + 8 * (lane >> 5);
-      bf16x8 bv[2];
+  for (int i = 0; i < FM; ++i)
+    a_at[i] = ((lane >> 5) * 8 + tr) * (BM * 2) + (piece_at<BM>((wm >> 5) + i, tr) << 6) + ((lane >> 4) & 1) * 32 +
+              (lane & 3) * 8;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) bv[j] = *reinterpret_cast<const bf16x8*>(&lds_b[wn + j * 32 + (lane & 31)][k]);
+  for (int j = 0; j < FN; ++j)
+    b_at[j] = kBytesA + ((lane >> 5) * 8 + tr) * (BN * 2) + (piece_at<BN>((wn >> 5) + j, tr) << 6) +
+              ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+
+  f32x16 acc[FM][FN];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const bf16x8 av = *reinterpret_cast<const bf16x8*>(&lds_a[n][wm + i * 32 + (lane & 31)][k]);
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av, bv[j], acc[i][j], 0, 0, 0);
-        }
+    for (int j = 0; j < FN; ++j) acc[i][j] = (f32x16)(0.0f);
+  const bool bias = a.db && n0 == 0 && wn == 0;
+  float bsum[FM] = {};
+
+  union Frag {
+    s16x4 h[2];
+    bf16x8 v;
+    uint32_t u[4];
+  };
+  Frag av[2][FM], bv[2][FN];
+  auto read4 = [&](int at) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(lds + at));
+  };
+  // The fragments' reads in the order in which the products need them: the
+  // first of A, all of B, the others of A; two halves each.
+  constexpr int kReads = 2 * (FM + FN), kMul = FM * FN;
+  auto read_piece = [&](int kk, int at, int r) {
+    const int f = r >> 1, h = r & 1;
+    if (f >= 1 && f <= FN) {
+      bv[kk][f - 1].h[h] = read4(at + b_at[f - 1] + (kk * 16 + h * 4) * (BN * 2));
+    } else {
+      const int i = f == 0 ? 0 : f - FN;
+      av[kk][i].h[h] = read4(at + a_at[i] + (kk * 16 + h * 4) * (BM * 2));
     }
-    __syncthreads();
+  };
+  // The products of fragments kk, with the reads of the next fragments
+  // between the first half of them and the loads between the second: a wave
+  // has its SIMD to itself, and whatever it issues in one piece leaves the
+  // matrix unit idle.
+  auto block = [&](int kk, int read_kk, int read_at, bool loads_a) {
+    constexpr int kHalf = kMul / 2;
+    constexpr int kPer = (kReads + kHalf - 1) / kHalf;
+    const int n_loads = loads_a ? LA : LB;
+    const int per_load = (n_loads + kHalf - 1) / kHalf;
+#pragma unroll
+    for (int q = 0; q < kMul; ++q) {
+      const int i = q / FN, j = q % FN;
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av[kk][i].v, bv[kk][j].v, acc[i][j], 0, 0, 0);
+#pragma unroll
+      for (int r = 0; r < kPer; ++r)
+        if (q < kHalf && q * kPer + r < kReads) read_piece(read_kk, read_at, q * kPer + r);
+#pragma unroll
+      for (int r = 0; r < per_load; ++r)
+        if (q >= kHalf && (q - kHalf) * per_load + r < n_loads) {
+          if (loads_a) {
+            load_a((q - kHalf) * per_load + r);
+          } else {
+            load_b((q - kHalf) * per_load + r);
+          }
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  auto add_bias = [&](int kk) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        bsum[i] += __uint_as_float(av[kk][i].u[h] << 16);
+        bsum[i] += __uint_as_float(av[kk][i].u[h] & 0xffff0000u);
+      }
+  };
+
+  // ---- the pipeline.  At the start of stage s stage s + 1 has arrived for
+  // every wave, so that its first fragments can be read while s is
+  // multiplied; stage s + kRing - 1 is loaded into the slot of s - 1, which
+  // every wave has read.
+  if (all > 0) {
+#pragma unroll
+    for (int p = 0; p < kRing - 1; ++p) {
+#pragma unroll
+      for (int i = 0; i < LA; ++i) load_a(i);
+#pragma unroll
+      for (int i = 0; i < LB; ++i) load_b(i);
+      advance();
+    }
+    wait_vm<(kRing - 2) * kLoads>();
+    lds_barrier();
+#pragma unroll
+    for (int r = 0; r < kReads; ++r) read_piece(0, 0, r);
+    int at = 0;
+    for (int s = 0; s < all; ++s) {
+      wait_vm<(kRing - 3) * kLoads>();
+      lds_barrier();
+      const int after = at + kStage == kRing * kStage ? 0 : at + kStage;
+      block(0, 1, at, true);
+      if (bias) add_bias(0);
+      block(1, 0, after, false);
+      if (bias) add_bias(1);
+      advance();
+      at = after;
+    }
+    wait_vm<0>();  // nothing may land in LDS that is no longer this workgroup's
   }
 
   // element e of a 32x32 accumulator: row 8*(e/4) + 4*(lane/32) + e%4, column lane%32
-  float* dw = a.dw + split * a.out * a.in;
+  float* dw = a.dw + (int64_t)split * a.out * a.in;
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int j = 0; j < FN; ++j) {
     const int64_t n = n0 + wn + j * 32 + (lane & 31);
     if (n >= a.in) continue;
     const float g = a.gain ? a.gain[n] : 1.0f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         const int64_t m = m0 + wm + i * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
@@ -145,92 +349,193 @@ __global__ void __launch_bounds__(256) wgrad_kernel(WgradArgs a) {
         *p = a.accumulate ? *p + v : v;
       }
   }
-  if (bias) {  // the four waves' sums, in wave order
-    float* red = reinterpret_cast<float*>(&lds_b[0][0]);
-    red[wave * 128 + 2 * lane] = bsum[0];
-    red[wave * 128 + 2 * lane + 1] = bsum[1];
-    __syncthreads();
-    const int64_t m = m0 + threadIdx.x;
-    if (threadIdx.x < kBM && m < a.out) {
-      const float v = ((red[threadIdx.x] + red[128 + threadIdx.x]) + red[256 + threadIdx.x]) + red[384 + threadIdx.x];
-      float* p = a.db + split * a.out + m;
-      *p = a.accumulate ? *p + v : v;
+  if (bias) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const float v = bsum[i] + __shfl_xor(bsum[i], 32, 64);  // the two halves of the rows
+      const int64_t m = m0 + wm + i * 32 + (lane & 31);
+      if (lane < 32 && m < a.out) {
+        float* p = a.db + (int64_t)split * a.out + m;
+        *p = a.accumulate ? *p + v : v;
+      }
     }
   }
 }
 
-// out[i] (+)= gain[i % in] * (the sum of the splits' partial sums, in order).
+// --------------------------------------------------------------------- join
+
+// out[i] (+)= gain[i % in] * (the sum of the splits' partial sums, in
+// order), and the same for the bias behind them.
 __global__ void __launch_bounds__(kThreads)
 join_kernel(const float* __restrict__ parts, int splits, int64_t n, int64_t in, const float* __restrict__ gain,
-            float* __restrict__ out, bool accumulate) {
+            float* __restrict__ out, const float* __restrict__ b_parts, int64_t n_bias, float* __restrict__ bias,
+            bool accumulate) {
   const int64_t step = (int64_t)gridDim.x * kThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
-    float s = parts[i];
-    for (int p = 1; p < splits; ++p) s += parts[(int64_t)p * n + i];
-    if (gain) s *= gain[i % in];
-    out[i] = accumulate ? out[i] + s : s;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n + n_bias; i += step) {
+    const bool b = i >= n;
+    const float* p = b ? b_parts + (i - n) : parts + i;
+    const int64_t stride = b ? n_bias : n;
+    float s = p[0];
+    for (int k = 1; k < splits; ++k) s += p[k * stride];
+    if (!b && gain) s *= gain[i % in];
+    float* o = b ? bias + (i - n) : out + i;
+    *o = accumulate ? *o + s : s;
   }
 }
 
-int64_t tiles(int64_t x, int64_t t) { return (x + t - 1) / t; }
+// --------------------------------------------------------------------- plan
 
-void launch_join(const float* parts, int splits, int64_t n, int64_t in, const float* gain, float* out,
-                 bool accumulate, hipStream_t s) {
-  int64_t grid = tiles(n, kThreads);
-  if (grid > 8192) grid = 8192;
-  join_kernel<<<(unsigned)grid, kThreads, 0, s>>>(parts, splits, n, in, gain, out, accumulate);
+// Tile shapes, and the time a CU takes for one row of a tile of each.
+struct Shape {
+  int bm, bn;
+  double row_ns;
+};
+constexpr Shape kShapes[] = {{256, 256, 24.0}, {256, 192, 18.5}, {256, 128, 13.0}, {128, 128, 8.5}};
+constexpr int kNumShapes = 4;
+constexpr int kCus = 256;
+constexpr int kMaxSplits = 32;
+constexpr int kMinSplitRows = 128;
+
+struct Plan {
+  int shape, splits;
+  int64_t split_rows;
+};
+
+// The tile shape and the number of splits with the least estimated time:
+// rounds of workgroups over the CUs, and for splits the partial sums written
+// and read again and one more launch.
+Plan wgrad_plan(int64_t rows, int64_t in, int64_t out) {
+  Plan best{0, 1, kBK};
+  double best_ns = 0.0;
+  for (int i = 0; i < kNumShapes; ++i) {
+    const int64_t t = ceil_div(out, kShapes[i].bm) * ceil_div(in, kShapes[i].bn);
+    for (int s = 1; s <= kMaxSplits; ++s) {
+      if (s > 1 && (rows < (int64_t)s * kMinSplitRows || t * (s - 1) >= 4 * kCus)) break;
+      const int64_t sr = ceil_div(ceil_div(rows, s), kBK) * kBK;
+      double ns = (double)ceil_div(t * s, kCus) * (double)sr * kShapes[i].row_ns;
+      if (s > 1) ns += 4000.0 + (double)(s + 1) * (double)out * (double)in * 4.0 / 5000.0;
+      if (best_ns == 0.0 || ns < best_ns) {
+        best_ns = ns;
+        best = Plan{i, s, sr < kBK ? kBK : sr};
+      }
+    }
+  }
+  return best;
+}
+
+// Whether the product reads this dy as it lies: bf16 rows of whole, aligned
+// 16-byte chunks whose stages span less than 2^32 bytes.
+bool direct(const scape_matrix& dy, int64_t out) {
+  return dy.dtype == SCAPE_BF16 && ((uintptr_t)dy.data & 15u) == 0 && dy.ld % 8 == 0 && out % 8 == 0 &&
+         dy.ld < (int64_t(1) << 25);
+}
+
+struct Layout {  // of the workspace, in bytes
+  bool as_it_lies;
+  int terms;
+  int64_t rows_pad, out_pad, t_first, t_rows;
+  size_t x, dy, parts, total;
+};
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+Layout layout_of(int64_t rows, int64_t in, int64_t out, const scape_matrix& dy, const Plan& p) {
+  Layout l;
+  l.as_it_lies = dy.data && direct(dy, out);
+  l.terms = dy.data ? terms_of(dy.dtype) : 3;
+  l.rows_pad = ceil_div(rows, kBK) * kBK;
+  l.out_pad = ceil_div(out, 8) * 8;
+  l.t_first = l.as_it_lies ? rows / kBK * kBK : 0;
+  l.t_rows = l.rows_pad - l.t_first;
+  l.x = 0;
+  l.dy = align256((size_t)l.rows_pad * (size_t)act_pitch(in) * 2);
+  l.parts = l.dy + align256((size_t)l.terms * (size_t)l.t_rows * (size_t)l.out_pad * 2);
+  l.total = l.parts + (p.splits == 1 ? 0 : align256((size_t)p.splits * (size_t)out * (size_t)(in + 1) * 4));
+  if (l.total == 0) l.total = 256;
+  return l;
+}
+
+template <int BM, int BN, int WM, int WN, int kRing>
+void launch_product(const WgradArgs& a, unsigned grid, hipStream_t s) {
+  wgrad_kernel<BM, BN, WM, WN, kRing><<<grid, kWaves * 64, 0, s>>>(a);
 }
 
 }  // namespace
 
-int wgrad_splits(int64_t rows, int64_t in, int64_t out) {
-  const int64_t t = tiles(out, kBM) * tiles(in, kBN);
-  int64_t s = (kTargetBlocks + t - 1) / t;
-  const int64_t most = rows / kMinSplitRows;
-  if (s > most) s = most;
-  return s < 1 ? 1 : (int)s;
-}
-
-size_t wgrad_workspace(int64_t rows, int64_t in, int64_t out) {
-  const int s = wgrad_splits(rows, in, out);
-  return s == 1 ? 256 : (size_t)s * (size_t)out * (size_t)(in + 1) * 4;
+size_t wgrad_workspace(int64_t rows, int64_t in, int64_t out, const scape_matrix& dy) {
+  return layout_of(rows, in, out, dy, wgrad_plan(rows, in, out)).total;
 }
 
 hipError_t launch_wgrad(int64_t rows, int64_t in, int64_t out, const scape_matrix& dy, const scape_act_view& x,
-                        const float* gain, float* dw, float* dbias, bool accumulate, float* ws, hipStream_t s) {
+                        const float* gain, float* dw, float* dbias, bool accumulate, void* ws, hipStream_t s) {
   if (rows < 1 && accumulate) return hipSuccess;
-  const int splits = wgrad_splits(rows, in, out);
+  const Plan plan = wgrad_plan(rows, in, out);
+  const Layout l = layout_of(rows, in, out, dy, plan);
+  char* const base = static_cast<char*>(ws);
+  hipError_t e = hipSuccess;
+  if (rows > 0) {
+    PrepArgs p{rows, l.rows_pad, act_blocks(in), out, l.out_pad, x.codes, x.scales,
+               reinterpret_cast<uint16_t*>(base + l.x), dy.data, dy.ld, reinterpret_cast<uint16_t*>(base + l.dy),
+               l.t_first, l.t_rows, 0};
+    int64_t xb = ceil_div(l.rows_pad * p.nblk * 4, kThreads), db = ceil_div(l.t_rows * (l.out_pad / 8), kThreads);
+    if (xb > 8192) xb = 8192;
+    if (db > 8192) db = 8192;
+    p.x_blocks = (unsigned)xb;
+    const unsigned grid = (unsigned)(xb + db);
+    switch (dy.dtype) {
+      case SCAPE_F32: wgrad_prepare_kernel<SCAPE_F32><<<grid, kThreads, 0, s>>>(p); break;
+      case SCAPE_BF16: wgrad_prepare_kernel<SCAPE_BF16><<<grid, kThreads, 0, s>>>(p); break;
+      case SCAPE_F16: wgrad_prepare_kernel<SCAPE_F16><<<grid, kThreads, 0, s>>>(p); break;
+    }
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  const int splits = plan.splits;
+  float* const parts = reinterpret_cast<float*>(base + l.parts);
   WgradArgs a{};
   a.rows = rows;
   a.in = in;
   a.out = out;
-  a.nblk = act_blocks(in);
-  a.dy = dy.data;
-  a.dy_ld = dy.ld;
-  a.codes = x.codes;
-  a.scales = x.scales;
-  a.split_rows = tiles(tiles(rows, splits), kBK) * kBK;
-  a.tiles_m = (int)tiles(out, kBM);
-  a.tiles_n = (int)tiles(in, kBN);
+  if (l.as_it_lies) {
+    a.a = static_cast<const char*>(dy.data);
+    a.a_step = dy.ld * 2;
+    a.a_cols = out;
+    a.terms = 1;
+    a.tail = l.t_rows ? base + l.dy : nullptr;
+  } else {
+    a.a = base + l.dy;
+    a.a_step = l.out_pad * 2;
+    a.a_plane = l.t_rows * l.out_pad * 2;
+    a.a_cols = l.out_pad;
+    a.terms = l.terms;
+  }
+  a.tail_step = l.out_pad * 2;
+  a.b = base + l.x;
+  a.b_step = act_pitch(in) * 2;
+  a.b_cols = act_pitch(in);
+  a.split_rows = plan.split_rows;
+  a.tiles_n = (int)ceil_div(in, kShapes[plan.shape].bn);
+  a.tiles = (int)(ceil_div(out, kShapes[plan.shape].bm) * a.tiles_n);
   if (splits == 1) {
     a.gain = gain;
     a.dw = dw;
     a.db = dbias;
     a.accumulate = accumulate;
   } else {
-    a.dw = ws;
-    a.db = dbias ? ws + (int64_t)splits * out * in : nullptr;
+    a.dw = parts;
+    a.db = dbias ? parts + (int64_t)splits * out * in : nullptr;
   }
-  const dim3 grid((unsigned)(a.tiles_m * (int64_t)a.tiles_n), (unsigned)splits);
-  switch (dy.dtype) {
-    case SCAPE_F32: wgrad_kernel<SCAPE_F32><<<grid, 256, 0, s>>>(a); break;
-    case SCAPE_BF16: wgrad_kernel<SCAPE_BF16><<<grid, 256, 0, s>>>(a); break;
-    case SCAPE_F16: wgrad_kernel<SCAPE_F16><<<grid, 256, 0, s>>>(a); break;
+  const unsigned grid = (unsigned)((int64_t)a.tiles * splits);
+  switch (plan.shape) {
+    case 0: launch_product<256, 256, 2, 2, 5>(a, grid, s); break;
+    case 1: launch_product<256, 192, 2, 2, 5>(a, grid, s); break;
+    case 2: launch_product<256, 128, 2, 2, 6>(a, grid, s); break;
+    case 3: launch_product<128, 128, 2, 2, 5>(a, grid, s); break;
   }
-  hipError_t e = hipGetLastError();
+  e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
-  launch_join(ws, splits, out * in, in, gain, dw, accumulate, s);
-  if (dbias) launch_join(a.db, splits, out, out, nullptr, dbias, accumulate, s);
+  const int64_t n = out * in, nb = dbias ? out : 0;
+  int64_t jb = ceil_div(n + nb, kThreads);
+  if (jb > 8192) jb = 8192;
+  join_kernel<<<(unsigned)jb, kThreads, 0, s>>>(parts, splits, n, in, gain, dw, a.db, nb, dbias, accumulate);
   return hipGetLastError();
 }
 

@@ -104,7 +104,7 @@ _SIGS = {
     "scape_rmsnorm_workspace_bytes": (c_size_t, [c_int64, c_int64]),
     "scape_rmsnorm_backward": (c_int, [c_int64, c_int64, Matrix, ActView, c_void_p, c_void_p, Matrix, Matrix,
                                        c_void_p, c_int32, c_void_p, c_size_t, c_void_p]),
-    "scape_wgrad_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64]),
+    "scape_wgrad_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64, Matrix]),
     "scape_wgrad": (c_int, [c_int64, c_int64, c_int64, Matrix, ActView, c_void_p, c_void_p, c_void_p, c_int32,
                             c_void_p, c_size_t, c_void_p]),
     "scape_status_string": (c_char_p, [c_int]),
@@ -637,8 +637,10 @@ def rmsnorm_backward(dy, xhat: ActCheckpoint, rstd, weight, dh, dweight, workspa
              ws, have)
 
 
-def wgrad_workspace_bytes(rows: int, n_in: int, n_out: int) -> int:
-    return int(lib().scape_wgrad_workspace_bytes(rows, n_in, n_out))
+def wgrad_workspace_bytes(rows: int, n_in: int, n_out: int, dy=None) -> int:
+    """Bytes of workspace of wgrad with this dy [rows][out], or with any."""
+    m = _NO_MATRIX if dy is None else _matrix(dy, "dy", rows, n_out, _device_of(dy, "dy"))
+    return int(lib().scape_wgrad_workspace_bytes(rows, n_in, n_out, m))
 
 
 def wgrad(dy, x: ActCheckpoint, dw, workspace, gain=None, dbias=None, accumulate: bool = False, stream=None) -> None:
@@ -649,10 +651,11 @@ def wgrad(dy, x: ActCheckpoint, dw, workspace, gain=None, dbias=None, accumulate
     dev = _device_of(dy, "dy")
     rows, n_out = dy.shape
     n_in = x.cols
-    ws, have = _workspace(workspace, wgrad_workspace_bytes(rows, n_in, n_out), dev)
+    m = _matrix(dy, "dy", rows, n_out, dev)
+    ws, have = _workspace(workspace, int(lib().scape_wgrad_workspace_bytes(rows, n_in, n_out, m)), dev)
     if dw is None:
         raise ValueError("dw is needed")
-    _enqueue(dev, stream, lib().scape_wgrad, rows, n_in, n_out, _matrix(dy, "dy", rows, n_out, dev),
+    _enqueue(dev, stream, lib().scape_wgrad, rows, n_in, n_out, m,
              _act(x, "x", rows, n_in, dev), _vector(gain, "gain", n_in, dev), _vector(dw, "dw", n_out * n_in, dev),
              _vector(dbias, "dbias", n_out, dev), 1 if accumulate else 0, ws, have)
 

@@ -35,6 +35,11 @@ def test_sizes():
         assert S.wgrad_workspace_bytes(rows, cols, 8) == 0 and S.wgrad_workspace_bytes(rows, 8, cols) == 0
     assert S.wgrad_workspace_bytes(4, 1 << 20, 1 << 20) == 0
     assert S.rmsnorm_workspace_bytes(4096, 1280) % 256 == 0
+    # the workspace for any dy covers each type's, aligned or not
+    L, most = S.lib(), S.wgrad_workspace_bytes(999, 100, 72)
+    sizes = [L.scape_wgrad_workspace_bytes(999, 100, 72, m)
+             for m in (mat(72), mat(73), mat(72, data=FAKE + 2), mat(72, 2), mat(72, 0))]
+    assert sizes[0] < sizes[1] == sizes[2] < sizes[3] < sizes[4] == most
     v = S.ActView()
     assert S.lib().scape_act_slot(8, 64, FAKE, ctypes.byref(v)) == 0
     assert v.codes == FAKE and v.scales == FAKE + 512
@@ -137,7 +142,8 @@ def wgrad_args(**kw):
     (dict(gain=FAKE + 2), INVALID),
     (dict(dbias=FAKE + 1), INVALID),
     (dict(workspace=None), INVALID),
-    (dict(nbytes=S.wgrad_workspace_bytes(4, 64, 64) - 1), WORKSPACE),
+    (dict(nbytes=S.lib().scape_wgrad_workspace_bytes(4, 64, 64, mat()) - 1), WORKSPACE),
+    (dict(dy=mat(dtype=0), nbytes=S.lib().scape_wgrad_workspace_bytes(4, 64, 64, mat())), WORKSPACE),
 ])
 def test_wgrad_refuses(kw, status):
     assert S.lib().scape_wgrad(*wgrad_args(**kw)) == status
