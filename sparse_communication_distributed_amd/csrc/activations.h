@@ -113,6 +113,47 @@ struct Elem<SCAPE_F16> {
   }
 };
 
+// The same 8 elements as they lie in memory, for loads that are kept under
+// way while something else is computed.
+template <int DT>
+struct Raw8 {
+  static constexpr int kWords = DT == SCAPE_F32 ? 8 : 4;
+  uint32_t u[kWords];
+  __device__ __forceinline__ void load(const void* p, int64_t row0, int64_t c, int64_t cols) {
+    const char* q = static_cast<const char*>(p) + (row0 + c) * (kWords / 2);
+    if (c + 8 <= cols) {
+      __builtin_memcpy(u, q, 16);
+      if (kWords == 8) __builtin_memcpy(u + kWords / 2, q + 16, 16);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) u[j] = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j < cols) {
+          if (kWords == 8) {
+            __builtin_memcpy(&u[j % kWords], q + 4 * j, 4);
+          } else {
+            uint16_t h;
+            __builtin_memcpy(&h, q + 2 * j, 2);
+            u[j / 2] |= (uint32_t)h << (16 * (j & 1));
+          }
+        }
+    }
+  }
+  __device__ __forceinline__ void unpack(float (&v)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (DT == SCAPE_F32) {
+        v[j] = __uint_as_float(u[j % kWords]);
+      } else if (DT == SCAPE_BF16) {
+        v[j] = __uint_as_float((j & 1) ? u[j / 2] & 0xffff0000u : u[j / 2] << 16);
+      } else {
+        v[j] = (float)__builtin_bit_cast(_Float16, (uint16_t)(u[j / 2] >> (16 * (j & 1))));
+      }
+    }
+  }
+};
+
 // Elements [c, c + 8) of a row of cols elements that starts at row0.
 template <int DT>
 __device__ __forceinline__ void load8(const void* p, int64_t row0, int64_t c, int64_t cols, float (&v)[8]) {

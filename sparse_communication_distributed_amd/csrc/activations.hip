@@ -5,6 +5,8 @@
 
 #include "activations.h"
 
+#include <type_traits>
+
 namespace scape {
 namespace {
 
@@ -77,7 +79,7 @@ unsigned walk_grid(int64_t rows, int64_t nblk) {
 
 // ---------------------------------------------------------------- RMS norm
 
-// Sum over the T threads (64: a wave; 256: the workgroup) that share a row;
+// Sum over the T threads (64: a wave; more: the workgroup) that share a row;
 // every thread gets it, the same one.
 template <typename V>
 __device__ __forceinline__ V wave_sum(V x) {
@@ -92,7 +94,10 @@ __device__ __forceinline__ V row_sum(V x, V* lds) {
   __syncthreads();  // the previous row's sum has been read
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
   __syncthreads();
-  return ((lds[0] + lds[1]) + lds[2]) + lds[3];
+  x = lds[0];
+#pragma unroll
+  for (int w = 1; w < T / 64; ++w) x += lds[w];
+  return x;
 }
 
 struct NormArgs {
@@ -158,10 +163,11 @@ __device__ __forceinline__ float norm_rstd(double sum, int64_t cols, float eps) 
 
 // Rows held in registers: T threads a row, C chunks of 8 columns a thread
 // (T * C * 8 >= cols).
+constexpr int group_of(int T) { return T == 64 ? kThreads : T; }  // threads of a workgroup
 template <int DT, int T, int C>
-__global__ void __launch_bounds__(kThreads) norm_kernel(NormArgs a) {
-  __shared__ double lds[4];
-  constexpr int kRows = kThreads / T;
+__global__ void __launch_bounds__(group_of(T)) norm_kernel(NormArgs a) {
+  __shared__ double lds[group_of(T) / 64];
+  constexpr int kRows = group_of(T) / T;
   const int t = threadIdx.x % T;
   for (int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / T; row < a.rows; row += (int64_t)gridDim.x * kRows) {
     float v[C][8];
@@ -251,42 +257,89 @@ __device__ __forceinline__ void back_emit(const NormBackArgs& a, int64_t row, in
   store8<DT>(a.dh, row * a.dh_ld, c, a.cols, o);
 }
 
-template <int DT, int T, int C>
-__global__ void __launch_bounds__(kThreads) norm_back_kernel(NormBackArgs a) {
-  __shared__ float lds[4];
-  __shared__ float part[T == 64 ? 64 * C * 8 : 1];
-  constexpr int kRows = kThreads / T;
-  const int t = threadIdx.x % T;
-  float dw[C][8];
-#pragma unroll
-  for (int i = 0; i < C; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
-  for (int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / T; row < a.rows; row += (int64_t)gridDim.x * kRows) {
-    float g[C][8], xh[C][8];
-    float sum = 0.0f;
+// One row's inputs of a thread, as they lie in memory.
+template <int DT, int C>
+struct BackRow {
+  Raw8<DT> dy[C], dres[C];
+  u32x2 codes[C];
+  uint32_t scale[C];
+  float rstd;
+  template <int T>
+  __device__ __forceinline__ void load(const NormBackArgs& a, int64_t row, int t) {
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int64_t c = (int64_t)(i * T + t) * 8;
-      load8<DT>(a.dy, row * a.dy_ld, c, a.cols, g[i]);
-      load_hat(a, row, c, xh[i]);
+      dy[i].load(a.dy, row * a.dy_ld, c, a.cols);
+      codes[i] = u32x2{0, 0};
+      scale[i] = 0;
+      if (c < a.nblk * kActBlock) {
+        const int64_t b = row * a.nblk + c / kActBlock;
+        codes[i] = *reinterpret_cast<const u32x2*>(a.codes + b * kActBlock + (c & 31));
+        scale[i] = a.scales[b];
+      }
+      if (a.dres) dres[i].load(a.dres, row * a.dres_ld, c, a.cols);
     }
+    rstd = a.rstd[row];
+  }
+};
+
+// T threads a row, C chunks of 8 columns a thread.  With one chunk the next
+// row is loaded while this one is computed (more would not fit the
+// registers of enough waves).  With dh in dy's or dres's place a row is read
+// whole before any of it is written, and no other thread reads it.
+template <int DT, int T, int C>
+__global__ void __launch_bounds__(group_of(T)) norm_back_kernel(NormBackArgs a) {
+  __shared__ float lds[group_of(T) / 64];
+  __shared__ float part[T == 64 ? 64 * C * 8 : 1];
+  constexpr int kRows = group_of(T) / T;
+  constexpr bool kAhead = C == 1;
+  const int t = threadIdx.x % T;
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  float dw[C][8], w[C][8];
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    load8<SCAPE_F32>(a.weight, 0, (int64_t)(i * T + t) * 8, a.cols, w[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+  }
+  int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / T;
+  BackRow<DT, C> next;
+  if (kAhead && row < a.rows) next.template load<T>(a, row, t);
+  for (; row < a.rows; row += step) {
+    if (!kAhead) next.template load<T>(a, row, t);
+    const BackRow<DT, C> cur = next;
+    if (kAhead && row + step < a.rows) next.template load<T>(a, row + step, t);
+    float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      float w[8];
-      load8<SCAPE_F32>(a.weight, 0, (int64_t)(i * T + t) * 8, a.cols, w);
+      float g[8], xh[8];
+      cur.dy[i].unpack(g);
+      act_decode(cur.codes[i], cur.scale[i], xh);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        dw[i][j] = __builtin_fmaf(g[i][j], xh[i][j], dw[i][j]);
-        g[i][j] *= w[j];
-        sum = __builtin_fmaf(g[i][j], xh[i][j], sum);
+        dw[i][j] = __builtin_fmaf(g[j], xh[j], dw[i][j]);
+        sum = __builtin_fmaf(g[j] * w[i][j], xh[j], sum);
       }
     }
     if (a.dh) {
       const float mean = row_sum<T>(sum, lds) / (float)a.cols;
-      const float rs = a.rstd[row];
 #pragma unroll
-      for (int i = 0; i < C; ++i) back_emit<DT>(a, row, (int64_t)(i * T + t) * 8, g[i], xh[i], mean, rs);
+      for (int i = 0; i < C; ++i) {
+        const int64_t c = (int64_t)(i * T + t) * 8;
+        if (c >= a.cols) continue;
+        float g[8], xh[8];
+        cur.dy[i].unpack(g);
+        act_decode(cur.codes[i], cur.scale[i], xh);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = cur.rstd * (g[j] * w[i][j] - xh[j] * mean);
+        if (a.dres) {
+          float r[8];
+          cur.dres[i].unpack(r);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) g[j] += r[j];
+        }
+        store8<DT>(a.dh, row * a.dh_ld, c, a.cols, g);
+      }
     }
   }
   if (!a.dw) return;
@@ -371,20 +424,25 @@ __global__ void __launch_bounds__(kThreads) norm_back_long_kernel(NormBackArgs a
   }
 }
 
-// out[c] (+)= the sum of parts[0 .. n)[c], 4 groups of parts a column, each
+// out[c] (+)= the sum of parts[0 .. n)[c]: 64 groups of parts a column, each
 // in order, then the groups in order.
-__global__ void __launch_bounds__(kThreads)
+constexpr int kSumCols = 16, kSumGroups = 64;
+__global__ void __launch_bounds__(kSumCols * kSumGroups)
 sum_parts_kernel(const float* __restrict__ parts, int64_t n, int64_t cols, float* __restrict__ out, bool accumulate) {
-  __shared__ float lds[4][64];
-  const int lane = threadIdx.x & 63, grp = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  __shared__ float lds[kSumGroups][kSumCols];
+  const int lane = threadIdx.x % kSumCols, grp = threadIdx.x / kSumCols;
+  const int64_t c = (int64_t)blockIdx.x * kSumCols + lane;
   float s = 0.0f;
-  if (c < cols)
-    for (int64_t p = grp; p < n; p += 4) s += parts[p * cols + c];
+  if (c < cols) {
+#pragma unroll 8
+    for (int64_t p = grp; p < n; p += kSumGroups) s += parts[p * cols + c];
+  }
   lds[grp][lane] = s;
   __syncthreads();
   if (grp == 0 && c < cols) {
-    s = ((lds[0][lane] + lds[1][lane]) + lds[2][lane]) + lds[3][lane];
+    s = lds[0][lane];
+#pragma unroll
+    for (int g = 1; g < kSumGroups; ++g) s += lds[g][lane];
     out[c] = accumulate ? out[c] + s : s;
   }
 }
@@ -394,53 +452,50 @@ __global__ void __launch_bounds__(kThreads) zero_f32_kernel(float* p, int64_t n)
   if (i < n) p[i] = 0.0f;
 }
 
-constexpr int64_t kWaveCols = 64 * 8 * 8;    // longest row one wave holds
-constexpr int64_t kGroupCols = 256 * 8 * 8;  // longest row one workgroup holds
-constexpr int64_t kBackBlocks = 512;
-
-template <int DT, int T>
-void norm_chunks(const NormArgs& a, unsigned grid, int64_t chunks, hipStream_t s) {
-  switch (chunks) {
-#define CASE(C) \
-  case C: norm_kernel<DT, T, C><<<grid, kThreads, 0, s>>>(a); break;
-    CASE(1) CASE(2) CASE(3) CASE(4) CASE(5) CASE(6) CASE(7) CASE(8)
-#undef CASE
-  }
-}
-
-template <int DT, int T>
-void back_chunks(const NormBackArgs& a, unsigned grid, int64_t chunks, hipStream_t s) {
-  switch (chunks) {
-#define CASE(C) \
-  case C: norm_back_kernel<DT, T, C><<<grid, kThreads, 0, s>>>(a); break;
-    CASE(1) CASE(2) CASE(3) CASE(4) CASE(5) CASE(6) CASE(7) CASE(8)
-#undef CASE
-  }
-}
+// Threads that share a row, and chunks of 8 columns a thread: a wave up to
+// 512 columns, workgroups of 128, 192 and 256 threads up to 2048 (one chunk
+// each; 256 threads for a row of 1280 columns took a tenth longer than 192),
+// then 256 and 1024 threads with one or two; longer rows are read twice.
+constexpr int64_t kWaveCols = 64 * 8, kGroupCols = 256 * 8 * 2, kWideCols = 1024 * 8 * 2;
+constexpr int64_t kBackBlocks = 1024;
 
 unsigned cap_grid(int64_t need, int64_t most) { return (unsigned)(need < most ? need : most); }
 
+template <typename F>
+void for_row_shape(int64_t cols, F&& f) {
+  if (cols <= 64 * 8) f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
+  else if (cols <= 128 * 8) f(std::integral_constant<int, 128>{}, std::integral_constant<int, 1>{});
+  else if (cols <= 192 * 8) f(std::integral_constant<int, 192>{}, std::integral_constant<int, 1>{});
+  else if (cols <= 256 * 8) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
+  else if (cols <= 256 * 16) f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
+  else if (cols <= 1024 * 8) f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 1>{});
+  else f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+}
+
 template <int DT>
 void norm_launch(const NormArgs& a, hipStream_t s) {
-  if (a.cols <= kWaveCols)
-    norm_chunks<DT, 64>(a, cap_grid((a.rows + 3) / 4, 65536), (a.cols + 511) / 512, s);
-  else if (a.cols <= kGroupCols)
-    norm_chunks<DT, 256>(a, cap_grid(a.rows, 65536), (a.cols + 2047) / 2048, s);
-  else
+  if (a.cols > kWideCols) {
     norm_long_kernel<DT><<<cap_grid(a.rows, 65536), kThreads, 0, s>>>(a);
+    return;
+  }
+  for_row_shape(a.cols, [&](auto t, auto c) {
+    constexpr int T = decltype(t)::value, C = decltype(c)::value, per = group_of(T) / T;
+    norm_kernel<DT, T, C><<<cap_grid((a.rows + per - 1) / per, 65536), group_of(T), 0, s>>>(a);
+  });
 }
 
 template <int DT>
 void back_launch(const NormBackArgs& a, unsigned parts, hipStream_t s) {
-  if (a.cols <= kWaveCols) {
-    back_chunks<DT, 64>(a, parts, (a.cols + 511) / 512, s);
-  } else if (a.cols <= kGroupCols) {
-    back_chunks<DT, 256>(a, parts, (a.cols + 2047) / 2048, s);
-  } else {
+  if (a.cols > kWideCols) {
     if (a.dw)
       norm_back_long_dw_kernel<DT><<<dim3(parts, (unsigned)((a.cols + 2047) / 2048)), kThreads, 0, s>>>(a);
     if (a.dh) norm_back_long_kernel<DT><<<cap_grid(a.rows, 65536), kThreads, 0, s>>>(a);
+    return;
   }
+  for_row_shape(a.cols, [&](auto t, auto c) {
+    constexpr int T = decltype(t)::value, C = decltype(c)::value;
+    norm_back_kernel<DT, T, C><<<parts, group_of(T), 0, s>>>(a);
+  });
 }
 
 }  // namespace
@@ -490,7 +545,8 @@ hipError_t launch_rmsnorm_pack(int64_t rows, int64_t cols, const scape_matrix& x
 int64_t rmsnorm_parts(int64_t rows, int64_t cols) {
   const int64_t per = cols <= kWaveCols ? 4 : 1;  // rows a workgroup works on at a time
   const int64_t need = (rows + per - 1) / per;
-  return need < 1 ? 1 : (need < kBackBlocks ? need : kBackBlocks);
+  const int64_t most = cols <= kGroupCols ? kBackBlocks : kBackBlocks / 4;
+  return need < 1 ? 1 : (need < most ? need : most);
 }
 
 hipError_t launch_rmsnorm_backward(int64_t rows, int64_t cols, const scape_matrix& dy, const scape_act_view& xhat,
@@ -516,7 +572,7 @@ hipError_t launch_rmsnorm_backward(int64_t rows, int64_t cols, const scape_matri
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !dweight || n == 1) return e;
-  sum_parts_kernel<<<(unsigned)((cols + 63) / 64), kThreads, 0, s>>>(parts, n, cols, dweight, accumulate);
+  sum_parts_kernel<<<(unsigned)((cols + kSumCols - 1) / kSumCols), kSumCols * kSumGroups, 0, s>>>(parts, n, cols, dweight, accumulate);
   return hipGetLastError();
 }
 
