@@ -507,7 +507,7 @@ scape_status scape_rmsnorm_backward(int64_t rows, int64_t cols, scape_matrix dy,
                                     hipStream_t stream);
 
 /* Bytes of scratch scape_wgrad needs with this dy (256-byte aligned): the
- * checkpoint as bf16, dy's bf16 terms (none for a bf16 dy of 16-byte aligned
+ * checkpoint in 16 bits, dy's terms (none for a 16-bit dy of 16-byte aligned
  * rows with out % 8 == 0) and partial sums.  dy.data null: enough for any dy.
  * 0 if a size is invalid. */
 size_t scape_wgrad_workspace_bytes(int64_t rows, int64_t in, int64_t out, scape_matrix dy);
@@ -519,9 +519,11 @@ size_t scape_wgrad_workspace_bytes(int64_t rows, int64_t in, int64_t out, scape_
  *   dw[o][i] = gain[i] * sum over rows of dy[r][o] * x[r][i]
  *   dbias[o] = sum over rows of dy[r][o]
  * added to what dw and dbias hold if accumulate is not 0.  gain null: 1.
- * dbias null: left out.  dw is contiguous.  Products of a bf16 dy are exact
- * and sums are fp32; dy of fp16 (fp32) is split into 2 (3) bf16 terms that
- * add up to it, so nothing of it is rounded away.
+ * dbias null: left out.  dw is contiguous.  Products are exact and sums are
+ * fp32: dy of fp32 is split into 3 bf16 terms that add up to it (below 2^-110
+ * a term may be lost), dy of fp16 is multiplied in fp16 by the checkpoint
+ * scaled to that type's range, in which values of the checkpoint are rounded
+ * only where their scale lies more than 2^32 below the checkpoint's largest.
  */
 scape_status scape_wgrad(int64_t rows, int64_t in, int64_t out, scape_matrix dy, scape_act_view x, const float* gain,
                          float* dw, float* dbias, int32_t accumulate, void* workspace, size_t workspace_bytes,

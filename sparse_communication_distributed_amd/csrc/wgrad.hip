@@ -2,12 +2,18 @@
 // dw[o][i] = gain[i] * sum_t dy[t][o] * x[t][i], on the matrix cores in bf16
 // with fp32 sums.  A checkpoint's values have at most 8 significant bits and
 // a power of two as their scale, so they are exact in bf16; a bf16 dy is
-// taken as it is, and fp16 and fp32 are split into 2 and 3 bf16 terms that
-// add up to the value.  So every product is exact and only the sums round.
+// taken as it is, and an fp32 one is split into 3 bf16 terms that add up to
+// the value.  So every product is exact and only the sums round.
 //
-// Launches: prepare (the checkpoint as bf16, and dy's terms where dy cannot
-// be read as it lies), the product over row splits, and with more than one
-// split the join of their partial sums.
+// An fp16 dy is multiplied in fp16 (two bf16 terms took twice the time).  The
+// checkpoint is then scaled by a power of two that brings its largest scale
+// to 2^8 (127 * 2^8 is in range), and the sums are scaled back: its values
+// are exact in fp16 down to 2^-32 times that scale, and smaller ones round
+// to multiples of 2^-24 before scaling back.
+//
+// Launches: for fp16 the largest scale; prepare (the checkpoint in 16 bits,
+// and dy's terms where dy cannot be read as it lies); the product over row
+// splits; with more than one split the join of their partial sums.
 
 #include "activations.h"
 
@@ -15,26 +21,61 @@ namespace scape {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) char lds_char;
 
 constexpr int kBK = 32;     // rows a stage
 constexpr int kWaves = 4;
-constexpr int terms_of(int dt) { return dt == SCAPE_F32 ? 3 : dt == SCAPE_F16 ? 2 : 1; }
+constexpr int terms_of(int dt) { return dt == SCAPE_F32 ? 3 : 1; }
 
 int64_t ceil_div(int64_t x, int64_t t) { return (x + t - 1) / t; }
 
 // ------------------------------------------------------------------ prepare
 
+// The largest finite scale byte, as kMaxParts partial maxima.
+constexpr int kMaxParts = 64;
+constexpr int kTopExp = 8;  // the largest scale becomes 2^kTopExp in fp16
+__global__ void __launch_bounds__(1024)
+scale_max_kernel(const uint8_t* __restrict__ scales, int64_t n, uint32_t* __restrict__ parts) {
+  __shared__ uint32_t lds[16];
+  uint32_t m = 0;
+  const int64_t step = (int64_t)kMaxParts * 1024 * 16;
+  for (int64_t i = ((int64_t)blockIdx.x * 1024 + threadIdx.x) * 16; i < n; i += step) {
+    uint8_t b[16];
+    if (i + 16 <= n) {
+      __builtin_memcpy(b, scales + i, 16);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) b[j] = i + j < n ? scales[i + j] : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) m = b[j] != 255 && b[j] > m ? b[j] : m;
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) {
+    const uint32_t o = __shfl_xor(m, d, 64);
+    m = o > m ? o : m;
+  }
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 16; ++w) m = lds[w] > m ? lds[w] : m;
+    parts[blockIdx.x] = m;
+  }
+}
+
 struct PrepArgs {
   int64_t rows, rows_pad, nblk, out, out_pad;
   const int8_t* codes;
   const uint8_t* scales;
-  uint16_t* x;  // [rows_pad][nblk * 32] bf16, zero past rows
+  uint16_t* x;  // [rows_pad][nblk * 32] bf16 (fp16 for an fp16 dy), zero past rows
+  const uint32_t* max_parts;  // fp16: the partial maxima of the scales
+  float* back;                // fp16: receives what the sums are multiplied by
   const void* dy;
   int64_t dy_ld;
-  // dy's terms [terms][t_rows][out_pad] bf16 of rows t_first .., zero past
+  // dy's terms [terms][t_rows][out_pad] in 16 bits of rows t_first .., zero past
   // dy's rows and columns: all rows, or the last, partial stage of a dy that
   // is read as it lies (none: t_rows = 0)
   uint16_t* terms;
@@ -61,13 +102,34 @@ __global__ void __launch_bounds__(kThreads) wgrad_prepare_kernel(PrepArgs a) {
   if (blockIdx.x < a.x_blocks) {
     const int64_t n = a.rows_pad * a.nblk * 4, step = (int64_t)a.x_blocks * kThreads;
     const int64_t full = a.rows * a.nblk * 4;
+    int shift = 0;  // of the scale byte
+    if (DT == SCAPE_F16) {
+      uint32_t m = a.max_parts[threadIdx.x & (kMaxParts - 1)];
+#pragma unroll
+      for (int d = 32; d >= 1; d >>= 1) {
+        const uint32_t o = __shfl_xor(m, d, 64);
+        m = o > m ? o : m;
+      }
+      shift = 127 + kTopExp - (int)m;
+      if (blockIdx.x == 0 && threadIdx.x == 0) *a.back = ldexpf(1.0f, -shift);
+    }
     for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
       u32x4 p = {0, 0, 0, 0};
       if (i < full) {
         float v[8];
-        act_decode(reinterpret_cast<const u32x2*>(a.codes)[i], a.scales[i >> 2], v);
+        const u32x2 q = reinterpret_cast<const u32x2*>(a.codes)[i];
+        const uint32_t s = a.scales[i >> 2];
+        if (DT == SCAPE_F16) {
+          const int e = (int)s + shift;  // under 1: less than any fp16 number
+          act_decode(q, s == 0 || s == 255 ? s : (e < 1 ? 0u : (uint32_t)e), v);
 #pragma unroll
-        for (int h = 0; h < 4; ++h) p[h] = upper_halves(__float_as_uint(v[2 * h]), __float_as_uint(v[2 * h + 1]));
+          for (int h = 0; h < 4; ++h)
+            p[h] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)v[2 * h], (_Float16)v[2 * h + 1]});
+        } else {
+          act_decode(q, s, v);
+#pragma unroll
+          for (int h = 0; h < 4; ++h) p[h] = upper_halves(__float_as_uint(v[2 * h]), __float_as_uint(v[2 * h + 1]));
+        }
       }
       reinterpret_cast<u32x4*>(a.x)[i] = p;
     }
@@ -84,8 +146,12 @@ __global__ void __launch_bounds__(kThreads) wgrad_prepare_kernel(PrepArgs a) {
       u32x4 p;
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
-        const uint32_t lo = cut_term(v[2 * h]), hi = cut_term(v[2 * h + 1]);
-        p[h] = upper_halves(lo, hi);
+        if (DT == SCAPE_F16) {
+          p[h] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)v[2 * h], (_Float16)v[2 * h + 1]});
+        } else {
+          const uint32_t lo = cut_term(v[2 * h]), hi = cut_term(v[2 * h + 1]);
+          p[h] = upper_halves(lo, hi);
+        }
       }
       *reinterpret_cast<u32x4*>(a.terms + (k * a.t_rows + r) * a.out_pad + c) = p;
     }
@@ -96,16 +162,17 @@ __global__ void __launch_bounds__(kThreads) wgrad_prepare_kernel(PrepArgs a) {
 
 struct WgradArgs {
   int64_t rows, in, out;
-  const char* a;         // dy or its terms: bf16 rows a_step bytes apart
+  const char* a;         // dy or its terms: 16-bit rows a_step bytes apart
   int64_t a_step;
   int64_t a_plane;       // bytes between terms
   int64_t a_cols;        // columns that may be read (a multiple of 8)
   int terms;
   const char* tail;      // the last, partial stage of a's rows, zero filled; null: none
   int64_t tail_step;
-  const char* b;         // the checkpoint as bf16, zero past rows to a whole stage
+  const char* b;         // the checkpoint in 16 bits, zero past rows to a whole stage
   int64_t b_step, b_cols;
-  const float* gain;     // applied here only when there is one split
+  const float* back;     // fp16: the sums' scale.  It and gain are applied here
+  const float* gain;     // only when there is one split
   float* dw;             // [splits][out][in], or dw itself (one split)
   float* db;             // [splits][out], or dbias itself; null: none
   bool accumulate;       // one split
@@ -132,7 +199,7 @@ __device__ __forceinline__ void wait_vm() {
   asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
 }
 
-// A stage of an operand lies in LDS as in memory, [row][W columns] of bf16.
+// A stage of an operand lies in LDS as in memory, [row][W columns] of 16 bits.
 // The 4 rows that a transposed read takes have to fall on different banks
 // (256 bytes hold all 64), so the 64-byte pieces of a row are permuted by
 // bits of the row number.
@@ -145,7 +212,7 @@ __device__ __forceinline__ int piece_at(int piece, int row) {
 // operands have the summed index (the rows) as their slow axis and come to
 // LDS as they lie, without a register; the transposed LDS read gives the
 // fragments.  A ring of kRing stages keeps kRing - 2 of them under way.
-template <int BM, int BN, int WM, int WN, int kRing>
+template <bool F16, int BM, int BN, int WM, int WN, int kRing>
 __global__ void __launch_bounds__(kWaves * 64) wgrad_kernel(WgradArgs a) {
   constexpr int FM = BM / WM / 32, FN = BN / WN / 32;
   constexpr int kBytesA = BM * kBK * 2, kStage = (BM + BN) * kBK * 2;
@@ -243,6 +310,7 @@ __global__ void __launch_bounds__(kWaves * 64) wgrad_kernel(WgradArgs a) {
   union Frag {
     s16x4 h[2];
     bf16x8 v;
+    f16x8 f;
     uint32_t u[4];
   };
   Frag av[2][FM], bv[2][FN];
@@ -273,7 +341,11 @@ __global__ void __launch_bounds__(kWaves * 64) wgrad_kernel(WgradArgs a) {
 #pragma unroll
     for (int q = 0; q < kMul; ++q) {
       const int i = q / FN, j = q % FN;
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av[kk][i].v, bv[kk][j].v, acc[i][j], 0, 0, 0);
+      if (F16) {
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(av[kk][i].f, bv[kk][j].f, acc[i][j], 0, 0, 0);
+      } else {
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av[kk][i].v, bv[kk][j].v, acc[i][j], 0, 0, 0);
+      }
 #pragma unroll
       for (int r = 0; r < kPer; ++r)
         if (q < kHalf && q * kPer + r < kReads) read_piece(read_kk, read_at, q * kPer + r);
@@ -294,8 +366,13 @@ __global__ void __launch_bounds__(kWaves * 64) wgrad_kernel(WgradArgs a) {
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
-        bsum[i] += __uint_as_float(av[kk][i].u[h] << 16);
-        bsum[i] += __uint_as_float(av[kk][i].u[h] & 0xffff0000u);
+        if (F16) {
+          bsum[i] += (float)av[kk][i].f[2 * h];
+          bsum[i] += (float)av[kk][i].f[2 * h + 1];
+        } else {
+          bsum[i] += __uint_as_float(av[kk][i].u[h] << 16);
+          bsum[i] += __uint_as_float(av[kk][i].u[h] & 0xffff0000u);
+        }
       }
   };
 
@@ -333,6 +410,7 @@ __global__ void __launch_bounds__(kWaves * 64) wgrad_kernel(WgradArgs a) {
 
   // element e of a 32x32 accumulator: row 8*(e/4) + 4*(lane/32) + e%4, column lane%32
   float* dw = a.dw + (int64_t)split * a.out * a.in;
+  const float back = F16 && a.back ? *a.back : 1.0f;
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
     const int64_t n = n0 + wn + j * 32 + (lane & 31);
@@ -345,7 +423,7 @@ __global__ void __launch_bounds__(kWaves * 64) wgrad_kernel(WgradArgs a) {
         const int64_t m = m0 + wm + i * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
         if (m >= a.out) continue;
         float* p = dw + m * a.in + n;
-        const float v = a.gain ? acc[i][j][e] * g : acc[i][j][e];
+        const float v = (F16 ? acc[i][j][e] * back : acc[i][j][e]) * g;
         *p = a.accumulate ? *p + v : v;
       }
   }
@@ -364,33 +442,52 @@ __global__ void __launch_bounds__(kWaves * 64) wgrad_kernel(WgradArgs a) {
 
 // --------------------------------------------------------------------- join
 
-// out[i] (+)= gain[i % in] * (the sum of the splits' partial sums, in
-// order), and the same for the bias behind them.
+// out[i] (+)= gain[i % in] * back * (the sum of the splits' partial sums, in
+// order), and for the bias behind them the plain sum.  VEC: 4 elements a
+// thread (in % 4 == 0, out 16-byte aligned).
+template <bool VEC>
 __global__ void __launch_bounds__(kThreads)
-join_kernel(const float* __restrict__ parts, int splits, int64_t n, int64_t in, const float* __restrict__ gain,
-            float* __restrict__ out, const float* __restrict__ b_parts, int64_t n_bias, float* __restrict__ bias,
-            bool accumulate) {
-  const int64_t step = (int64_t)gridDim.x * kThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n + n_bias; i += step) {
-    const bool b = i >= n;
-    const float* p = b ? b_parts + (i - n) : parts + i;
-    const int64_t stride = b ? n_bias : n;
-    float s = p[0];
-    for (int k = 1; k < splits; ++k) s += p[k * stride];
-    if (!b && gain) s *= gain[i % in];
-    float* o = b ? bias + (i - n) : out + i;
-    *o = accumulate ? *o + s : s;
+join_kernel(const float* __restrict__ parts, int splits, int64_t n, int64_t in, const float* __restrict__ back,
+            const float* __restrict__ gain, float* __restrict__ out, const float* __restrict__ b_parts,
+            int64_t n_bias, float* __restrict__ bias, bool accumulate) {
+  constexpr int V = VEC ? 4 : 1;
+  const int64_t step = (int64_t)gridDim.x * kThreads, tid = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const float k = back ? *back : 1.0f;
+  for (int64_t i = tid * V; i < n; i += step * V) {
+    float s[V];
+    __builtin_memcpy(s, __builtin_assume_aligned(parts + i, 4 * V), 4 * V);
+    for (int p = 1; p < splits; ++p) {
+      float q[V];
+      __builtin_memcpy(q, __builtin_assume_aligned(parts + p * n + i, 4 * V), 4 * V);
+#pragma unroll
+      for (int j = 0; j < V; ++j) s[j] += q[j];
+    }
+    const int64_t c = !gain ? 0 : n < (int64_t(1) << 32) ? (int64_t)((uint32_t)i % (uint32_t)in) : i % in;
+    float* o = out + i;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      s[j] *= k;
+      if (gain) s[j] *= gain[c + j];
+      if (accumulate) s[j] = o[j] + s[j];
+    }
+    __builtin_memcpy(__builtin_assume_aligned(o, 4 * V), s, 4 * V);
+  }
+  for (int64_t i = tid; i < n_bias; i += step) {
+    float s = b_parts[i];
+    for (int p = 1; p < splits; ++p) s += b_parts[p * n_bias + i];
+    bias[i] = accumulate ? bias[i] + s : s;
   }
 }
 
 // --------------------------------------------------------------------- plan
 
-// Tile shapes, and the time a CU takes for one row of a tile of each.
+// Tile shapes, and the time in ns that a CU was measured to take for one row
+// of a tile of each (all CUs at work).
 struct Shape {
   int bm, bn;
   double row_ns;
 };
-constexpr Shape kShapes[] = {{256, 256, 24.0}, {256, 192, 18.5}, {256, 128, 13.0}, {128, 128, 8.5}};
+constexpr Shape kShapes[] = {{256, 256, 28.0}, {256, 192, 23.5}, {256, 128, 21.0}, {128, 128, 14.5}};
 constexpr int kNumShapes = 4;
 constexpr int kCus = 256;
 constexpr int kMaxSplits = 32;
@@ -403,8 +500,8 @@ struct Plan {
 
 // The tile shape and the number of splits with the least estimated time:
 // rounds of workgroups over the CUs, and for splits the partial sums written
-// and read again and one more launch.
-Plan wgrad_plan(int64_t rows, int64_t in, int64_t out) {
+// and read again (5 TB/s) and one more launch.
+Plan wgrad_plan(int64_t rows, int64_t in, int64_t out, int terms) {
   Plan best{0, 1, kBK};
   double best_ns = 0.0;
   for (int i = 0; i < kNumShapes; ++i) {
@@ -412,7 +509,7 @@ Plan wgrad_plan(int64_t rows, int64_t in, int64_t out) {
     for (int s = 1; s <= kMaxSplits; ++s) {
       if (s > 1 && (rows < (int64_t)s * kMinSplitRows || t * (s - 1) >= 4 * kCus)) break;
       const int64_t sr = ceil_div(ceil_div(rows, s), kBK) * kBK;
-      double ns = (double)ceil_div(t * s, kCus) * (double)sr * kShapes[i].row_ns;
+      double ns = (double)ceil_div(t * s, kCus) * (double)(sr * terms) * kShapes[i].row_ns;
       if (s > 1) ns += 4000.0 + (double)(s + 1) * (double)out * (double)in * 4.0 / 5000.0;
       if (best_ns == 0.0 || ns < best_ns) {
         best_ns = ns;
@@ -423,10 +520,10 @@ Plan wgrad_plan(int64_t rows, int64_t in, int64_t out) {
   return best;
 }
 
-// Whether the product reads this dy as it lies: bf16 rows of whole, aligned
+// Whether the product reads this dy as it lies: 16-bit rows of whole, aligned
 // 16-byte chunks whose stages span less than 2^32 bytes.
 bool direct(const scape_matrix& dy, int64_t out) {
-  return dy.dtype == SCAPE_BF16 && ((uintptr_t)dy.data & 15u) == 0 && dy.ld % 8 == 0 && out % 8 == 0 &&
+  return dy.dtype != SCAPE_F32 && ((uintptr_t)dy.data & 15u) == 0 && dy.ld % 8 == 0 && out % 8 == 0 &&
          dy.ld < (int64_t(1) << 25);
 }
 
@@ -434,48 +531,67 @@ struct Layout {  // of the workspace, in bytes
   bool as_it_lies;
   int terms;
   int64_t rows_pad, out_pad, t_first, t_rows;
-  size_t x, dy, parts, total;
+  size_t max, x, dy, parts, total;
 };
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 Layout layout_of(int64_t rows, int64_t in, int64_t out, const scape_matrix& dy, const Plan& p) {
   Layout l;
-  l.as_it_lies = dy.data && direct(dy, out);
-  l.terms = dy.data ? terms_of(dy.dtype) : 3;
+  l.as_it_lies = direct(dy, out);
+  l.terms = terms_of(dy.dtype);
   l.rows_pad = ceil_div(rows, kBK) * kBK;
   l.out_pad = ceil_div(out, 8) * 8;
   l.t_first = l.as_it_lies ? rows / kBK * kBK : 0;
   l.t_rows = l.rows_pad - l.t_first;
-  l.x = 0;
-  l.dy = align256((size_t)l.rows_pad * (size_t)act_pitch(in) * 2);
+  l.max = 0;  // kMaxParts words, then the float `back`
+  l.x = 512;
+  l.dy = l.x + align256((size_t)l.rows_pad * (size_t)act_pitch(in) * 2);
   l.parts = l.dy + align256((size_t)l.terms * (size_t)l.t_rows * (size_t)l.out_pad * 2);
   l.total = l.parts + (p.splits == 1 ? 0 : align256((size_t)p.splits * (size_t)out * (size_t)(in + 1) * 4));
-  if (l.total == 0) l.total = 256;
   return l;
 }
 
-template <int BM, int BN, int WM, int WN, int kRing>
-void launch_product(const WgradArgs& a, unsigned grid, hipStream_t s) {
-  wgrad_kernel<BM, BN, WM, WN, kRing><<<grid, kWaves * 64, 0, s>>>(a);
+template <bool F16>
+void launch_product(const WgradArgs& a, int shape, unsigned grid, hipStream_t s) {
+  switch (shape) {
+    case 0: wgrad_kernel<F16, 256, 256, 2, 2, 5><<<grid, kWaves * 64, 0, s>>>(a); break;
+    case 1: wgrad_kernel<F16, 256, 192, 2, 2, 5><<<grid, kWaves * 64, 0, s>>>(a); break;
+    case 2: wgrad_kernel<F16, 256, 128, 2, 2, 6><<<grid, kWaves * 64, 0, s>>>(a); break;
+    case 3: wgrad_kernel<F16, 128, 128, 2, 2, 5><<<grid, kWaves * 64, 0, s>>>(a); break;
+  }
 }
 
 }  // namespace
 
 size_t wgrad_workspace(int64_t rows, int64_t in, int64_t out, const scape_matrix& dy) {
-  return layout_of(rows, in, out, dy, wgrad_plan(rows, in, out)).total;
+  if (dy.data) return layout_of(rows, in, out, dy, wgrad_plan(rows, in, out, terms_of(dy.dtype))).total;
+  size_t most = 0;  // of any type, aligned or not
+  for (int dt : {SCAPE_F32, SCAPE_BF16, SCAPE_F16}) {
+    const scape_matrix m{reinterpret_cast<void*>(uintptr_t(4)), out, dt};  // not 16-byte aligned
+    const size_t t = wgrad_workspace(rows, in, out, m);
+    most = t > most ? t : most;
+  }
+  return most;
 }
 
 hipError_t launch_wgrad(int64_t rows, int64_t in, int64_t out, const scape_matrix& dy, const scape_act_view& x,
                         const float* gain, float* dw, float* dbias, bool accumulate, void* ws, hipStream_t s) {
   if (rows < 1 && accumulate) return hipSuccess;
-  const Plan plan = wgrad_plan(rows, in, out);
+  const bool f16 = dy.dtype == SCAPE_F16;
+  const Plan plan = wgrad_plan(rows, in, out, terms_of(dy.dtype));
   const Layout l = layout_of(rows, in, out, dy, plan);
   char* const base = static_cast<char*>(ws);
+  uint32_t* const max_parts = reinterpret_cast<uint32_t*>(base + l.max);
+  float* const back = f16 && rows > 0 ? reinterpret_cast<float*>(max_parts + kMaxParts) : nullptr;
   hipError_t e = hipSuccess;
   if (rows > 0) {
+    if (f16) {
+      scale_max_kernel<<<kMaxParts, 1024, 0, s>>>(x.scales, rows * act_blocks(in), max_parts);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
     PrepArgs p{rows, l.rows_pad, act_blocks(in), out, l.out_pad, x.codes, x.scales,
-               reinterpret_cast<uint16_t*>(base + l.x), dy.data, dy.ld, reinterpret_cast<uint16_t*>(base + l.dy),
-               l.t_first, l.t_rows, 0};
+               reinterpret_cast<uint16_t*>(base + l.x), max_parts, back, dy.data, dy.ld,
+               reinterpret_cast<uint16_t*>(base + l.dy), l.t_first, l.t_rows, 0};
     int64_t xb = ceil_div(l.rows_pad * p.nblk * 4, kThreads), db = ceil_div(l.t_rows * (l.out_pad / 8), kThreads);
     if (xb > 8192) xb = 8192;
     if (db > 8192) db = 8192;
@@ -515,6 +631,7 @@ hipError_t launch_wgrad(int64_t rows, int64_t in, int64_t out, const scape_matri
   a.tiles_n = (int)ceil_div(in, kShapes[plan.shape].bn);
   a.tiles = (int)(ceil_div(out, kShapes[plan.shape].bm) * a.tiles_n);
   if (splits == 1) {
+    a.back = back;
     a.gain = gain;
     a.dw = dw;
     a.db = dbias;
@@ -524,18 +641,21 @@ hipError_t launch_wgrad(int64_t rows, int64_t in, int64_t out, const scape_matri
     a.db = dbias ? parts + (int64_t)splits * out * in : nullptr;
   }
   const unsigned grid = (unsigned)((int64_t)a.tiles * splits);
-  switch (plan.shape) {
-    case 0: launch_product<256, 256, 2, 2, 5>(a, grid, s); break;
-    case 1: launch_product<256, 192, 2, 2, 5>(a, grid, s); break;
-    case 2: launch_product<256, 128, 2, 2, 6>(a, grid, s); break;
-    case 3: launch_product<128, 128, 2, 2, 5>(a, grid, s); break;
+  if (f16) {
+    launch_product<true>(a, plan.shape, grid, s);
+  } else {
+    launch_product<false>(a, plan.shape, grid, s);
   }
   e = hipGetLastError();
   if (e != hipSuccess || splits == 1) return e;
   const int64_t n = out * in, nb = dbias ? out : 0;
-  int64_t jb = ceil_div(n + nb, kThreads);
+  const bool vec = in % 4 == 0 && ((uintptr_t)dw & 15u) == 0;
+  int64_t jb = ceil_div(vec ? n / 4 : n, kThreads);
   if (jb > 8192) jb = 8192;
-  join_kernel<<<(unsigned)jb, kThreads, 0, s>>>(parts, splits, n, in, gain, dw, a.db, nb, dbias, accumulate);
+  if (vec)
+    join_kernel<true><<<(unsigned)jb, kThreads, 0, s>>>(parts, splits, n, in, back, gain, dw, a.db, nb, dbias, accumulate);
+  else
+    join_kernel<false><<<(unsigned)jb, kThreads, 0, s>>>(parts, splits, n, in, back, gain, dw, a.db, nb, dbias, accumulate);
   return hipGetLastError();
 }
 

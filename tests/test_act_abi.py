@@ -39,7 +39,8 @@ def test_sizes():
     L, most = S.lib(), S.wgrad_workspace_bytes(999, 100, 72)
     sizes = [L.scape_wgrad_workspace_bytes(999, 100, 72, m)
              for m in (mat(72), mat(73), mat(72, data=FAKE + 2), mat(72, 2), mat(72, 0))]
-    assert sizes[0] < sizes[1] == sizes[2] < sizes[3] < sizes[4] == most
+    assert sizes[0] < sizes[1] == sizes[2] <= sizes[4] == most
+    assert L.scape_wgrad_workspace_bytes(999, 100, 72, mat(73, 2)) <= most
     v = S.ActView()
     assert S.lib().scape_act_slot(8, 64, FAKE, ctypes.byref(v)) == 0
     assert v.codes == FAKE and v.scales == FAKE + 512

@@ -372,6 +372,45 @@ def test_wgrad_values(S, rows, n_in, n_out, dt):
     assert torch.equal(dw, dw2)
 
 
+@pytest.mark.parametrize("lead", [0, 3])
+def test_wgrad_fp16_range(S, lead):
+    """Subnormal fp16 gradients (multiples of 2^-24), and blocks whose scales
+    lie 2^30 apart: still exact.  Only scales more than 2^32 below the
+    checkpoint's largest round, by less than 2^-33 of it."""
+    rows, n_in, n_out = 30, 96, 40
+    r = np.random.default_rng(3)
+    q = r.integers(-127, 128, (rows, n_in)).astype(np.int8)
+    s = np.tile(np.array([150, 120, 111], dtype=np.uint8), (rows, 1))
+    dyn = r.integers(-1023, 1024, (rows, n_out)) * 2.0 ** -24
+    dy = Guarded(rows, n_out, torch.float16, 0, lead, dyn)
+    assert np.array_equal(f32(dy.t), dyn.astype(np.float32))
+    ws = torch.empty(S.wgrad_workspace_bytes(rows, n_in, n_out, dy.t), dtype=torch.uint8, device=DEV)
+    dw, db = torch.empty(n_out, n_in, device=DEV), torch.empty(n_out, device=DEV)
+    S.wgrad(dy.t, fill_act(S, q, s, n_in), dw, ws, dbias=db)
+    want, wb = A.wgrad(dyn, A.unpack(q, s, n_in))
+    got = f32(dw)
+    assert np.array_equal(got[:, :64], want[:, :64].astype(np.float32))
+    assert np.array_equal(f32(db), wb.astype(np.float32))
+    # a value is off by at most half of 2^-24 (scaled), each at one gradient
+    within(got[:, 64:], want[:, 64:], 2.0 ** (150 - 135 - 25) * np.abs(dyn).sum(axis=0)[:, None] * 1.001, "small block")
+
+
+def test_wgrad_other_workspace_sizes(S):
+    """A workspace of exactly the size asked for this dy, dirty."""
+    for dt in DT:
+        for rows, n_in, n_out, lead in ((999, 100, 72, 0), (999, 100, 72, 1), (640, 64, 64, 0), (3000, 40, 33, 0)):
+            q, s, dyn = exact_inputs(rows, n_in, n_out, dt, 7)
+            dy = Guarded(rows, n_out, DT[dt], 0, lead, dyn)
+            need = S.wgrad_workspace_bytes(rows, n_in, n_out, dy.t)
+            assert need <= S.wgrad_workspace_bytes(rows, n_in, n_out)
+            buf = torch.full((need + 512,), 0xFF, dtype=torch.uint8, device=DEV)
+            dw, db = torch.empty(n_out, n_in, device=DEV), torch.empty(n_out, device=DEV)
+            S.wgrad(dy.t, fill_act(S, q, s, n_in), dw, buf[:need], dbias=db)
+            want, wb = A.wgrad(dyn, A.unpack(q, s, n_in))
+            assert np.array_equal(f32(dw), want.astype(np.float32)) and np.array_equal(f32(db), wb.astype(np.float32))
+            assert (buf[need:] == 0xFF).all()
+
+
 def test_wgrad_nonfinite(S):
     q, s, dyn = exact_inputs(64, 64, 40, "bf16", 5)
     for dt in DT:
