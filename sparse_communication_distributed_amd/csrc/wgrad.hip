@@ -408,24 +408,36 @@ __global__ void __launch_bounds__(kWaves * 64) wgrad_kernel(WgradArgs a) {
     wait_vm<0>();  // nothing may land in LDS that is no longer this workgroup's
   }
 
-  // element e of a 32x32 accumulator: row 8*(e/4) + 4*(lane/32) + e%4, column lane%32
-  float* dw = a.dw + (int64_t)split * a.out * a.in;
+  // Element e of a 32x32 accumulator: row 8*(e/4) + 4*(lane/32) + e%4, column
+  // lane%32.  The address is a uniform row start and the lane's offset.
   const float back = F16 && a.back ? *a.back : 1.0f;
+  const int64_t m_first = m0 + wm, n_first = n0 + wn;
+  const uint32_t lane_off = (uint32_t)(4 * (lane >> 5) * a.in + (lane & 31));
+  const int64_t rows_left = a.out - m_first - 4 * (lane >> 5), cols_left = a.in - n_first - (lane & 31);
+  float* const dw = a.dw + (int64_t)split * a.out * a.in + m_first * a.in + n_first;
+  auto store_tile = [&](auto whole, auto adds) {
 #pragma unroll
-  for (int j = 0; j < FN; ++j) {
-    const int64_t n = n0 + wn + j * 32 + (lane & 31);
-    if (n >= a.in) continue;
-    const float g = a.gain ? a.gain[n] : 1.0f;
+    for (int j = 0; j < FN; ++j) {
+      const bool col = whole.value || j * 32 < cols_left;
+      const float g = a.gain && col ? (a.gain + n_first + j * 32)[lane & 31] : 1.0f;
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+      for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int64_t m = m0 + wm + i * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-        if (m >= a.out) continue;
-        float* p = dw + m * a.in + n;
-        const float v = (F16 ? acc[i][j][e] * back : acc[i][j][e]) * g;
-        *p = a.accumulate ? *p + v : v;
-      }
+        for (int e = 0; e < 16; ++e) {
+          const int m = i * 32 + 8 * (e >> 2) + (e & 3);
+          float* const p = dw + m * a.in + j * 32;
+          const float v = (F16 ? acc[i][j][e] * back : acc[i][j][e]) * g;
+          if (whole.value || (col && m < rows_left)) p[lane_off] = adds.value ? p[lane_off] + v : v;
+        }
+    }
+  };
+  const bool whole = m0 + BM <= a.out && n0 + BN <= a.in;
+  if (a.accumulate) {
+    store_tile(std::false_type{}, std::true_type{});
+  } else if (whole) {
+    store_tile(std::true_type{}, std::false_type{});
+  } else {
+    store_tile(std::false_type{}, std::false_type{});
   }
   if (bias) {
 #pragma unroll
