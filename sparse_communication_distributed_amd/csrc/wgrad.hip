@@ -311,7 +311,8 @@ __global__ void __launch_bounds__(kWaves * 64) wgrad_kernel(WgradArgs a) {
     s16x4 h[2];
     bf16x8 v;
     f16x8 f;
-    uint32_t u[4];
+    bf16x2 b2[4];
+    f16x2 f2[4];
   };
   Frag av[2][FM], bv[2][FN];
   auto read4 = [&](int at) {
@@ -366,12 +367,11 @@ __global__ void __launch_bounds__(kWaves * 64) wgrad_kernel(WgradArgs a) {
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
+        // one fused sum of two elements times one and the sum so far
         if (F16) {
-          bsum[i] += (float)av[kk][i].f[2 * h];
-          bsum[i] += (float)av[kk][i].f[2 * h + 1];
+          bsum[i] = __builtin_amdgcn_fdot2(av[kk][i].f2[h], f16x2{(_Float16)1.0f, (_Float16)1.0f}, bsum[i], false);
         } else {
-          bsum[i] += __uint_as_float(av[kk][i].u[h] << 16);
-          bsum[i] += __uint_as_float(av[kk][i].u[h] & 0xffff0000u);
+          bsum[i] = __builtin_amdgcn_fdot2_f32_bf16(av[kk][i].b2[h], bf16x2{(__bf16)1.0f, (__bf16)1.0f}, bsum[i], false);
         }
       }
   };
@@ -493,36 +493,48 @@ join_kernel(const float* __restrict__ parts, int splits, int64_t n, int64_t in, 
 
 // --------------------------------------------------------------------- plan
 
-// Tile shapes, and the time in ns that a CU was measured to take for one row
-// of a tile of each (all CUs at work).
+// Tile shapes, and the time in ns that a round of them over the CUs was
+// measured to take a row (all CUs at work; two 128x128 tiles share a CU).
 struct Shape {
   int bm, bn;
-  double row_ns;
+  double row_ns, pair_ns;  // one tile a CU; two (0: they do not fit)
 };
-constexpr Shape kShapes[] = {{256, 256, 28.0}, {256, 192, 23.5}, {256, 128, 21.0}, {128, 128, 14.5}};
+constexpr Shape kShapes[] = {{256, 256, 23.3, 0.0}, {256, 192, 19.1, 0.0}, {256, 128, 13.4, 0.0}, {128, 128, 8.6, 14.3}};
 constexpr int kNumShapes = 4;
 constexpr int kCus = 256;
 constexpr int kMaxSplits = 32;
 constexpr int kMinSplitRows = 128;
+constexpr double kBytesPerNs = 5000.0;  // of partial sums and results
+constexpr double kRoundNs = 5000.0, kLaunchNs = 4000.0;
 
 struct Plan {
   int shape, splits;
   int64_t split_rows;
 };
 
-// The tile shape and the number of splits with the least estimated time:
-// rounds of workgroups over the CUs, and for splits the partial sums written
-// and read again (5 TB/s) and one more launch.
+// The tile shape and the number of splits with the least estimated time: the
+// rounds of workgroups, the tiles written, and for splits the partial sums
+// read again and one more launch.
 Plan wgrad_plan(int64_t rows, int64_t in, int64_t out, int terms) {
   Plan best{0, 1, kBK};
   double best_ns = 0.0;
   for (int i = 0; i < kNumShapes; ++i) {
-    const int64_t t = ceil_div(out, kShapes[i].bm) * ceil_div(in, kShapes[i].bn);
+    const Shape& sh = kShapes[i];
+    const int64_t t = ceil_div(out, sh.bm) * ceil_div(in, sh.bn);
     for (int s = 1; s <= kMaxSplits; ++s) {
       if (s > 1 && (rows < (int64_t)s * kMinSplitRows || t * (s - 1) >= 4 * kCus)) break;
       const int64_t sr = ceil_div(ceil_div(rows, s), kBK) * kBK;
-      double ns = (double)ceil_div(t * s, kCus) * (double)(sr * terms) * kShapes[i].row_ns;
-      if (s > 1) ns += 4000.0 + (double)(s + 1) * (double)out * (double)in * 4.0 / 5000.0;
+      const double work = (double)(sr * terms), bytes = (double)out * (double)in * 4.0;
+      double ns;
+      if (sh.pair_ns > 0.0) {
+        const int64_t full = t * s / (2 * kCus), rest = t * s - full * 2 * kCus;
+        ns = (double)full * (work * sh.pair_ns + kRoundNs);
+        if (rest) ns += work * (rest <= kCus ? sh.row_ns : sh.pair_ns) + kRoundNs;
+      } else {
+        ns = (double)ceil_div(t * s, kCus) * (work * sh.row_ns + kRoundNs);
+      }
+      ns += (double)s * bytes / kBytesPerNs;
+      if (s > 1) ns += kLaunchNs + (double)(s + 1) * bytes / kBytesPerNs;
       if (best_ns == 0.0 || ns < best_ns) {
         best_ns = ns;
         best = Plan{i, s, sr < kBK ? kBK : sr};
