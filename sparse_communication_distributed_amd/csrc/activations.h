@@ -114,14 +114,15 @@ struct Elem<SCAPE_F16> {
 };
 
 // The same 8 elements as they lie in memory, for loads that are kept under
-// way while something else is computed.
-template <int DT>
+// way while something else is computed.  With WHOLE a chunk past the row is
+// the row's last one.
+template <int DT, bool WHOLE>
 struct Raw8 {
   static constexpr int kWords = DT == SCAPE_F32 ? 8 : 4;
   uint32_t u[kWords];
   __device__ __forceinline__ void load(const void* p, int64_t row0, int64_t c, int64_t cols) {
-    const char* q = static_cast<const char*>(p) + (row0 + c) * (kWords / 2);
-    if (c + 8 <= cols) {
+    const char* q = static_cast<const char*>(p) + (row0 + (!WHOLE || c < cols ? c : cols - 8)) * (kWords / 2);
+    if (WHOLE || c + 8 <= cols) {
       __builtin_memcpy(u, q, 16);
       if (kWords == 8) __builtin_memcpy(u + kWords / 2, q + 16, 16);
     } else {
@@ -154,21 +155,28 @@ struct Raw8 {
   }
 };
 
-// Elements [c, c + 8) of a row of cols elements that starts at row0.
-template <int DT>
+// Elements [c, c + 8) of a row of cols elements that starts at row0.  WHOLE:
+// cols is a multiple of 8, so a chunk is all there or not at all, and one
+// past the row is loaded from the row's end and set to zero: no branch, behind
+// which the compiler would wait for every load under way.
+template <int DT, bool WHOLE = false>
 __device__ __forceinline__ void load8(const void* p, int64_t row0, int64_t c, int64_t cols, float (&v)[8]) {
-  if (c + 8 <= cols) {
+  if (WHOLE) {
+    Elem<DT>::load(p, row0 + (c < cols ? c : cols - 8), v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c < cols ? v[j] : 0.0f;
+  } else if (c + 8 <= cols) {
     Elem<DT>::load(p, row0 + c, v);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? Elem<DT>::get(p, row0 + c + j) : 0.0f;
   }
 }
-template <int DT>
+template <int DT, bool WHOLE = false>
 __device__ __forceinline__ void store8(void* p, int64_t row0, int64_t c, int64_t cols, const float (&v)[8]) {
-  if (c + 8 <= cols) {
+  if (WHOLE ? c < cols : c + 8 <= cols) {
     Elem<DT>::store(p, row0 + c, v);
-  } else {
+  } else if (!WHOLE) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (c + j < cols) Elem<DT>::put(p, row0 + c + j, v[j]);

@@ -117,30 +117,30 @@ struct NormArgs {
   float* rstd;
 };
 
-template <int DT>
+template <int DT, bool WHOLE = false>
 __device__ __forceinline__ void load_sum(const NormArgs& a, int64_t row, int64_t c, float (&v)[8]) {
-  load8<DT>(a.x, row * a.x_ld, c, a.cols, v);
+  load8<DT, WHOLE>(a.x, row * a.x_ld, c, a.cols, v);
   if (a.res) {
     float r[8];
-    load8<DT>(a.res, row * a.res_ld, c, a.cols, r);
+    load8<DT, WHOLE>(a.res, row * a.res_ld, c, a.cols, r);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += r[j];
   }
 }
 
 // h, y and the code of one lane's 8 columns (a quad writes one scale).
-template <int DT>
+template <int DT, bool WHOLE = false>
 __device__ __forceinline__ void norm_emit(const NormArgs& a, int64_t row, int64_t c, const float (&v)[8], float rs) {
-  if (a.h && c < a.cols) store8<DT>(a.h, row * a.h_ld, c, a.cols, v);
+  if (a.h && c < a.cols) store8<DT, WHOLE>(a.h, row * a.h_ld, c, a.cols, v);
   float xh[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) xh[j] = v[j] * rs;
   if (a.y && c < a.cols) {
     float w[8];
-    load8<SCAPE_F32>(a.weight, 0, c, a.cols, w);
+    load8<SCAPE_F32, WHOLE>(a.weight, 0, c, a.cols, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[j] = xh[j] * w[j];
-    store8<DT>(a.y, row * a.y_ld, c, a.cols, w);
+    store8<DT, WHOLE>(a.y, row * a.y_ld, c, a.cols, w);
   }
   if (a.codes) {
     const uint32_t amax = quad_max(act_amax8(xh));
@@ -164,7 +164,7 @@ __device__ __forceinline__ float norm_rstd(double sum, int64_t cols, float eps) 
 // Rows held in registers: T threads a row, C chunks of 8 columns a thread
 // (T * C * 8 >= cols).
 constexpr int group_of(int T) { return T == 64 ? kThreads : T; }  // threads of a workgroup
-template <int DT, int T, int C>
+template <int DT, int T, int C, bool WHOLE>
 __global__ void __launch_bounds__(group_of(T)) norm_kernel(NormArgs a) {
   __shared__ double lds[group_of(T) / 64];
   constexpr int kRows = group_of(T) / T;
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(group_of(T)) norm_kernel(NormArgs a) {
     double s = 0.0;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      load_sum<DT>(a, row, (int64_t)(i * T + t) * 8, v[i]);
+      load_sum<DT, WHOLE>(a, row, (int64_t)(i * T + t) * 8, v[i]);
     }
 #pragma unroll
     for (int i = 0; i < C; ++i)
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(group_of(T)) norm_kernel(NormArgs a) {
     const float rs = norm_rstd(s, a.cols, a.eps);
     if (a.rstd && t == 0) a.rstd[row] = rs;
 #pragma unroll
-    for (int i = 0; i < C; ++i) norm_emit<DT>(a, row, (int64_t)(i * T + t) * 8, v[i], rs);
+    for (int i = 0; i < C; ++i) norm_emit<DT, WHOLE>(a, row, (int64_t)(i * T + t) * 8, v[i], rs);
   }
 }
 
@@ -258,9 +258,9 @@ __device__ __forceinline__ void back_emit(const NormBackArgs& a, int64_t row, in
 }
 
 // One row's inputs of a thread, as they lie in memory.
-template <int DT, int C>
+template <int DT, int C, bool WHOLE>
 struct BackRow {
-  Raw8<DT> dy[C], dres[C];
+  Raw8<DT, WHOLE> dy[C], dres[C];
   u32x2 codes[C];
   uint32_t scale[C];
   float rstd;
@@ -270,13 +270,10 @@ struct BackRow {
     for (int i = 0; i < C; ++i) {
       const int64_t c = (int64_t)(i * T + t) * 8;
       dy[i].load(a.dy, row * a.dy_ld, c, a.cols);
-      codes[i] = u32x2{0, 0};
-      scale[i] = 0;
-      if (c < a.nblk * kActBlock) {
-        const int64_t b = row * a.nblk + c / kActBlock;
-        codes[i] = *reinterpret_cast<const u32x2*>(a.codes + b * kActBlock + (c & 31));
-        scale[i] = a.scales[b];
-      }
+      // past the row: its last codes, whose products are left out of the sum
+      const int64_t at = c < a.nblk * kActBlock ? c : a.nblk * kActBlock - 8;
+      codes[i] = *reinterpret_cast<const u32x2*>(a.codes + row * a.nblk * kActBlock + at);
+      scale[i] = a.scales[row * a.nblk + at / kActBlock];
       if (a.dres) dres[i].load(a.dres, row * a.dres_ld, c, a.cols);
     }
     rstd = a.rstd[row];
@@ -287,7 +284,7 @@ struct BackRow {
 // row is loaded while this one is computed (more would not fit the
 // registers of enough waves).  With dh in dy's or dres's place a row is read
 // whole before any of it is written, and no other thread reads it.
-template <int DT, int T, int C>
+template <int DT, int T, int C, bool WHOLE>
 __global__ void __launch_bounds__(group_of(T)) norm_back_kernel(NormBackArgs a) {
   __shared__ float lds[group_of(T) / 64];
   __shared__ float part[T == 64 ? 64 * C * 8 : 1];
@@ -298,28 +295,30 @@ __global__ void __launch_bounds__(group_of(T)) norm_back_kernel(NormBackArgs a) 
   float dw[C][8], w[C][8];
 #pragma unroll
   for (int i = 0; i < C; ++i) {
-    load8<SCAPE_F32>(a.weight, 0, (int64_t)(i * T + t) * 8, a.cols, w[i]);
+    load8<SCAPE_F32, WHOLE>(a.weight, 0, (int64_t)(i * T + t) * 8, a.cols, w[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
   }
   int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / T;
-  BackRow<DT, C> next;
+  BackRow<DT, C, WHOLE> next;
   if (kAhead && row < a.rows) next.template load<T>(a, row, t);
   for (; row < a.rows; row += step) {
     if (!kAhead) next.template load<T>(a, row, t);
-    const BackRow<DT, C> cur = next;
-    if (kAhead && row + step < a.rows) next.template load<T>(a, row + step, t);
+    const BackRow<DT, C, WHOLE> cur = next;
+    if (kAhead) next.template load<T>(a, row + step < a.rows ? row + step : row, t);
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       float g[8], xh[8];
       cur.dy[i].unpack(g);
       act_decode(cur.codes[i], cur.scale[i], xh);
+      float s = sum;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         dw[i][j] = __builtin_fmaf(g[j], xh[j], dw[i][j]);
-        sum = __builtin_fmaf(g[j] * w[i][j], xh[j], sum);
+        s = __builtin_fmaf(g[j] * w[i][j], xh[j], s);
       }
+      sum = (int64_t)(i * T + t) * 8 < a.cols ? s : sum;
     }
     if (a.dh) {
       const float mean = row_sum<T>(sum, lds) / (float)a.cols;
@@ -338,7 +337,7 @@ __global__ void __launch_bounds__(group_of(T)) norm_back_kernel(NormBackArgs a) 
 #pragma unroll
           for (int j = 0; j < 8; ++j) g[j] += r[j];
         }
-        store8<DT>(a.dh, row * a.dh_ld, c, a.cols, g);
+        store8<DT, WHOLE>(a.dh, row * a.dh_ld, c, a.cols, g);
       }
     }
   }
@@ -480,7 +479,11 @@ void norm_launch(const NormArgs& a, hipStream_t s) {
   }
   for_row_shape(a.cols, [&](auto t, auto c) {
     constexpr int T = decltype(t)::value, C = decltype(c)::value, per = group_of(T) / T;
-    norm_kernel<DT, T, C><<<cap_grid((a.rows + per - 1) / per, 65536), group_of(T), 0, s>>>(a);
+    const unsigned grid = cap_grid((a.rows + per - 1) / per, 65536);
+    if (a.cols % 8 == 0)
+      norm_kernel<DT, T, C, true><<<grid, group_of(T), 0, s>>>(a);
+    else
+      norm_kernel<DT, T, C, false><<<grid, group_of(T), 0, s>>>(a);
   });
 }
 
@@ -494,7 +497,10 @@ void back_launch(const NormBackArgs& a, unsigned parts, hipStream_t s) {
   }
   for_row_shape(a.cols, [&](auto t, auto c) {
     constexpr int T = decltype(t)::value, C = decltype(c)::value;
-    norm_back_kernel<DT, T, C><<<parts, group_of(T), 0, s>>>(a);
+    if (a.cols % 8 == 0)
+      norm_back_kernel<DT, T, C, true><<<parts, group_of(T), 0, s>>>(a);
+    else
+      norm_back_kernel<DT, T, C, false><<<parts, group_of(T), 0, s>>>(a);
   });
 }
 
