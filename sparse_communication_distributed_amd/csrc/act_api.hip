@@ -39,6 +39,13 @@ scape_status check_act(const char* name, const scape_act_view& a, int64_t rows, 
 
 bool misaligned4(const void* p) { return ((uintptr_t)p & 3u) != 0; }
 
+scape_status check_workspace(const void* ws, size_t have, size_t need) {
+  if (!ws) return fail(SCAPE_EINVAL, "workspace is null");
+  if ((uintptr_t)ws & 255u) return fail(SCAPE_EINVAL, "workspace must be 256-byte aligned");
+  if (have < need) return fail(SCAPE_EWORKSPACE, "workspace has %zu bytes, needs %zu", have, need);
+  return SCAPE_OK;
+}
+
 // An output may be an input's own matrix, element on element, or lie apart.
 bool shifted_alias(const scape_matrix& o, const scape_matrix& i, int64_t rows) {
   return o.data && o.data == i.data && rows > 1 && o.ld != i.ld;
@@ -134,10 +141,7 @@ scape_status scape_rmsnorm_backward(int64_t rows, int64_t cols, scape_matrix dy,
     return fail(SCAPE_EINVAL, "dres and dh must have dy's dtype");
   if (shifted_alias(dh, dy, rows) || shifted_alias(dh, dres, rows))
     return fail(SCAPE_EINVAL, "an output in an input's place must have its ld");
-  const size_t need = scape_rmsnorm_workspace_bytes(rows, cols);
-  if (!workspace) return fail(SCAPE_EINVAL, "workspace is null");
-  if (workspace_bytes < need)
-    return fail(SCAPE_EWORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+  if ((st = check_workspace(workspace, workspace_bytes, scape_rmsnorm_workspace_bytes(rows, cols)))) return st;
   return hip_check(launch_rmsnorm_backward(rows, cols, dy, xhat, rstd, weight, dres, dh, dweight, accumulate != 0,
                                            static_cast<float*>(workspace), stream),
                    "rmsnorm backward");
@@ -161,10 +165,7 @@ scape_status scape_wgrad(int64_t rows, int64_t in, int64_t out, scape_matrix dy,
   if (!dw) return fail(SCAPE_EINVAL, "dw is null");
   if (misaligned4(gain) || misaligned4(dw) || misaligned4(dbias))
     return fail(SCAPE_EINVAL, "gain, dw and dbias must be 4-byte aligned");
-  const size_t need = wgrad_workspace(rows, in, out, dy);
-  if (!workspace) return fail(SCAPE_EINVAL, "workspace is null");
-  if (workspace_bytes < need)
-    return fail(SCAPE_EWORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+  if ((st = check_workspace(workspace, workspace_bytes, wgrad_workspace(rows, in, out, dy)))) return st;
   return hip_check(launch_wgrad(rows, in, out, dy, x, gain, dw, dbias, accumulate != 0, workspace, stream),
                    "wgrad");
 }

@@ -117,6 +117,7 @@ def back_args(**kw):
     (dict(dh=mat(ld=72)), INVALID),  # in dy's place with another ld
     (dict(dres=mat(ld=63)), SHAPE),
     (dict(workspace=None), INVALID),
+    (dict(workspace=FAKE + 16), INVALID),
     (dict(nbytes=S.rmsnorm_workspace_bytes(4, 64) - 1), WORKSPACE),
 ])
 def test_rmsnorm_backward_refuses(kw, status):
@@ -143,6 +144,7 @@ def wgrad_args(**kw):
     (dict(gain=FAKE + 2), INVALID),
     (dict(dbias=FAKE + 1), INVALID),
     (dict(workspace=None), INVALID),
+    (dict(workspace=FAKE + 128), INVALID),
     (dict(nbytes=S.lib().scape_wgrad_workspace_bytes(4, 64, 64, mat()) - 1), WORKSPACE),
     (dict(dy=mat(dtype=0), nbytes=S.lib().scape_wgrad_workspace_bytes(4, 64, 64, mat())), WORKSPACE),
 ])

@@ -162,7 +162,7 @@ def test_pack_many_rows_and_far_offsets(S):
 # ---------------------------------------------------------------- RMS norm
 
 NORM_SHAPES = [(1, 1), (3, 31), (5, 33), (1, 2048), (9, 777), (67, 1280), (6, 4096), (5, 4097), (3, 5632), (2, 16384),
-               (2, 16421), (2300, 520)]
+               (2, 16421), (2300, 520), (5, 8), (33, 1024), (9, 1536), (4, 2056), (3, 8192), (2, 8200)]
 
 
 @pytest.mark.parametrize("dt", list(DT))
@@ -301,6 +301,27 @@ def test_rmsnorm_backward_places(S, cols):
     within(one, f32(one).astype(np.float64), 0.0, "finite")
 
 
+@pytest.mark.parametrize("cols", [200, 1280, 4096, 8192, 777])
+def test_rmsnorm_backward_nonfinite(S, cols):
+    """An infinity in a row's last column reaches that row and its column of
+    dweight and nothing else (threads past a row's end read its last chunk)."""
+    rows = 9
+    g = torch.Generator(DEV).manual_seed(5)
+    x, dy = (torch.randn(rows, cols, device=DEV, dtype=torch.bfloat16, generator=g) for _ in range(2))
+    w = torch.ones(cols, device=DEV)
+    y, a, rstd = torch.empty_like(x), S.act_alloc(rows, cols, DEV), torch.empty(rows, device=DEV)
+    S.rmsnorm_pack(x, w, EPS, y, xhat=a, rstd=rstd)
+    ws = torch.empty(S.rmsnorm_workspace_bytes(rows, cols), dtype=torch.uint8, device=DEV)
+    dh, dw = torch.empty_like(x), torch.empty(cols, device=DEV)
+    S.rmsnorm_backward(dy, a, rstd, w, dh, dw, ws)
+    dy[4, cols - 1] = float("inf")
+    dh2, dw2 = torch.empty_like(x), torch.empty(cols, device=DEV)
+    S.rmsnorm_backward(dy, a, rstd, w, dh2, dw2, ws)
+    keep = [r for r in range(rows) if r != 4]
+    assert torch.equal(dh2[keep], dh[keep]) and not torch.isfinite(dh2[4]).any()
+    assert torch.equal(dw2[:-1], dw[:-1]) and torch.isinf(dw2[-1])
+
+
 # ----------------------------------------------------------- weight gradient
 
 WGRAD_SHAPES = [(1, 1, 1), (1, 64, 64), (7, 33, 5), (31, 32, 130), (64, 777, 129), (257, 129, 257), (33, 520, 1531),
@@ -393,6 +414,40 @@ def test_wgrad_fp16_range(S, lead):
     assert np.array_equal(f32(db), wb.astype(np.float32))
     # a value is off by at most half of 2^-24 (scaled), each at one gradient
     within(got[:, 64:], want[:, 64:], 2.0 ** (150 - 135 - 25) * np.abs(dyn).sum(axis=0)[:, None] * 1.001, "small block")
+
+
+@pytest.mark.parametrize("ld", [(1 << 25) - 8, (1 << 25) + 8, (1 << 26) + 1])
+def test_wgrad_far_rows(S, ld):
+    """Rows of dy as far apart as the product reads them in place, further,
+    and past 2^32 elements in all."""
+    rows, n_in, n_out = 70, 40, 24
+    q, s, dyn = exact_inputs(rows, n_in, n_out, "bf16", 12)
+    buf = torch.empty(rows * ld, dtype=torch.bfloat16, device=DEV)
+    dy = buf.view(rows, ld)[:, :n_out]
+    dy.copy_(torch.from_numpy(dyn))
+    ws = torch.empty(S.wgrad_workspace_bytes(rows, n_in, n_out, dy), dtype=torch.uint8, device=DEV)
+    dw, db = torch.empty(n_out, n_in, device=DEV), torch.empty(n_out, device=DEV)
+    S.wgrad(dy, fill_act(S, q, s, n_in), dw, ws, dbias=db)
+    want, wb = A.wgrad(dyn, A.unpack(q, s, n_in))
+    assert np.array_equal(f32(dw), want.astype(np.float32)) and np.array_equal(f32(db), wb.astype(np.float32))
+
+
+@pytest.mark.parametrize("rows,n_in,n_out", [(40, 4096, 4096), (64, 1536, 8192), (96, 1024, 8192), (2500, 520, 640),
+                                             (300, 2048, 2048)])
+def test_wgrad_tile_shapes(S, rows, n_in, n_out):
+    """Sizes that take each tile shape, with and without splits."""
+    for dt in ("bf16", "fp16"):
+        q, s, dyn = exact_inputs(rows, n_in, n_out, dt, 13)
+        a, dy = fill_act(S, q, s, n_in), torch.from_numpy(dyn).to(DEV, DT[dt])
+        x = torch.from_numpy(A.unpack(q, s, n_in)).to(DEV)
+        want = dy.double().t().contiguous() @ x  # exact: sums of whole numbers
+        ws = torch.empty(S.wgrad_workspace_bytes(rows, n_in, n_out, dy), dtype=torch.uint8, device=DEV)
+        dw, db = torch.empty(n_out, n_in, device=DEV), torch.empty(n_out, device=DEV)
+        gain = torch.full((n_in,), 0.5, device=DEV)
+        S.wgrad(dy, a, dw, ws, gain=gain, dbias=db)
+        assert torch.equal(dw.double() * 2, want) and torch.equal(db.double(), dy.double().sum(0))
+        S.wgrad(dy, a, dw, ws, dbias=db, accumulate=True)
+        assert torch.equal(dw.double() * 2, want * 3)
 
 
 def test_wgrad_other_workspace_sizes(S):
