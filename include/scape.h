@@ -33,6 +33,8 @@
  *   - Arithmetic: IEEE binary32, each operation rounded separately (no
  *     contraction), correctly rounded sqrt and division, subnormals kept.
  *     Results are deterministic and match the CPU oracle bit for bit.
+ *     (The activation operators have limits and arithmetic of their own,
+ *     stated there.)
  */
 #ifndef SCAPE_H
 #define SCAPE_H

@@ -97,6 +97,7 @@ __device__ __forceinline__ uint32_t upper_halves(uint32_t a, uint32_t b) {
   return __builtin_amdgcn_perm(b, a, 0x07060302u);
 }
 
+// Bound by memory: [16384][2048] codes to bf16 18 us (102 MB, 5.6 TB/s).
 template <int DT>
 __global__ void __launch_bounds__(kThreads) wgrad_prepare_kernel(PrepArgs a) {
   if (blockIdx.x < a.x_blocks) {
@@ -208,6 +209,15 @@ __device__ __forceinline__ int piece_at(int piece, int row) {
   return W == 192 ? piece ^ ((row >> 1) & 1) : piece ^ (row & 3);
 }
 
+// 16384 rows, 2048 -> 5632, bf16: 315-375 us for 378 GFLOP (1.0-1.2 PFLOP/s;
+// the library's product of the same bf16 operands takes 412 us), 8192 rows,
+// 4096 -> 4096: 210-230 us (1.2-1.3).  With the loads left out the first takes
+// 295, with everything but the loads left out 260: it is held by the products
+// (whose clock falls with the data's power: all-zero inputs take 278) and by
+// the latency of loads that miss the XCD's L2.  Two waves a SIMD instead of
+// one, blocks of tiles for each XCD, and loads issued earlier or more evenly
+// took the same time or more.
+//
 // One workgroup sums a BM x BN tile of dw over the rows of one split.  Both
 // operands have the summed index (the rows) as their slow axis and come to
 // LDS as they lie, without a register; the transposed LDS read gives the
@@ -456,7 +466,8 @@ __global__ void __launch_bounds__(kWaves * 64) wgrad_kernel(WgradArgs a) {
 
 // out[i] (+)= gain[i % in] * back * (the sum of the splits' partial sums, in
 // order), and for the bias behind them the plain sum.  VEC: 4 elements a
-// thread (in % 4 == 0, out 16-byte aligned).
+// thread (in % 4 == 0, out 16-byte aligned).  5 splits of 1280 x 1280: 8.7 us
+// (39 MB, 4.5 TB/s).
 template <bool VEC>
 __global__ void __launch_bounds__(kThreads)
 join_kernel(const float* __restrict__ parts, int splits, int64_t n, int64_t in, const float* __restrict__ back,

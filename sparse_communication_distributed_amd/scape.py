@@ -518,12 +518,12 @@ def _matrix(t, name: str, rows: int, cols: int, device: int) -> Matrix:
     if _DTYPES is None:
         import torch
         _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-    if t.get_device() != device or not t.is_cuda:
+    if t.get_device() != device:  # -1: host memory
         raise ValueError(f"{name} must be a tensor on device {device} (got {t.device})")
     dt = _DTYPES.get(t.dtype)
     if dt is None:
         raise ValueError(f"{name} must be float32, bfloat16 or float16 (got {t.dtype})")
-    if tuple(t.shape) != (rows, cols):
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must have shape ({rows}, {cols}) (got {tuple(t.shape)})")
     ld, one = t.stride()
     if cols > 1 and one != 1:
@@ -540,7 +540,7 @@ def _vector(t, name: str, numel: int, device: int) -> Optional[int]:
     if t is None:
         return None
     import torch
-    if t.get_device() != device or not t.is_cuda or t.dtype != torch.float32:
+    if t.get_device() != device or t.dtype != torch.float32:
         raise ValueError(f"{name} must be a float32 tensor on device {device} (got {t.dtype} on {t.device})")
     if not t.is_contiguous() or t.numel() != numel:
         raise ValueError(f"{name} must be contiguous with {numel} elements (got {tuple(t.shape)})")
@@ -557,7 +557,7 @@ def _act(a, name: str, rows: int, cols: int, device: int) -> ActView:
 
 
 def _workspace(t, need: int, device: int):
-    if t.get_device() != device or not t.is_cuda or not t.is_contiguous():
+    if t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on device {device}")
     have = t.numel() * t.element_size()
     if have < need:
