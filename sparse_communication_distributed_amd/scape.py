@@ -547,9 +547,16 @@ def _vector(t, name: str, numel: int, device: int) -> Optional[int]:
     return t.data_ptr()
 
 
+def _checkpoint(a, name: str) -> ActCheckpoint:
+    if not isinstance(a, ActCheckpoint):
+        raise ValueError(f"{name} must be an ActCheckpoint (got {type(a).__name__})")
+    return a
+
+
 def _act(a, name: str, rows: int, cols: int, device: int) -> ActView:
     if a is None:
         return _NO_ACT
+    _checkpoint(a, name)
     if a.device != device or a.rows != rows or a.cols != cols:
         raise ValueError(f"{name} must be a checkpoint of ({rows}, {cols}) on device {device} "
                          f"(got ({a.rows}, {a.cols}) on device {a.device})")
@@ -575,19 +582,28 @@ def _device_of(t, name: str) -> int:
     return t.get_device()
 
 
+_raw_stream = None  # device -> handle of its current stream
+
+
 def _enqueue(device: int, stream, fn, *args) -> None:
     """Calls fn(*args, stream) with `device` current: on the given stream,
     which has to be that device's, or on the device's current one."""
+    global _raw_stream
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device.index != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors are on device {device}")
+    if stream is not None:
+        if stream.device.index != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on device {device}")
+        handle = stream.cuda_stream
+    else:
+        if _raw_stream is None:  # without the Stream object, a sixth of a small call's time
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                  lambda d: torch.cuda.current_stream(d).cuda_stream)
+        handle = _raw_stream(device)
     if torch.cuda.current_device() == device:
-        _check(fn(*args, stream.cuda_stream))
+        _check(fn(*args, handle))
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, stream.cuda_stream))
+            _check(fn(*args, handle))
 
 
 def act_pack(x, out: ActCheckpoint, stream=None) -> None:
@@ -600,7 +616,7 @@ def act_pack(x, out: ActCheckpoint, stream=None) -> None:
 
 def act_unpack(a: ActCheckpoint, out, gain=None, stream=None) -> None:
     """out [rows][cols] = the checkpoint's values (times gain[cols])."""
-    dev, rows, cols = a.device, a.rows, a.cols
+    dev, rows, cols = _checkpoint(a, "a").device, a.rows, a.cols
     _enqueue(dev, stream, lib().scape_act_unpack, rows, cols, a.view, _vector(gain, "gain", cols, dev),
              _matrix(out, "out", rows, cols, dev))
 
@@ -650,7 +666,7 @@ def wgrad(dy, x: ActCheckpoint, dw, workspace, gain=None, dbias=None, accumulate
     dbias may be parts of a row of the optimizer's gradients."""
     dev = _device_of(dy, "dy")
     rows, n_out = dy.shape
-    n_in = x.cols
+    n_in = _checkpoint(x, "x").cols
     m = _matrix(dy, "dy", rows, n_out, dev)
     ws, have = _workspace(workspace, int(lib().scape_wgrad_workspace_bytes(rows, n_in, n_out, m)), dev)
     if dw is None:

@@ -522,7 +522,7 @@ def test_binding_refuses(S):
                 lambda: S.rmsnorm_backward(x, a, rstd, w, x, w, ws[:8]),
                 lambda: S.rmsnorm_backward(x, a, rstd, w, x, w, ws[8:]),
                 lambda: S.wgrad(x, a, dw[:, :32], ws), lambda: S.wgrad(x, a, dw.half(), ws),
-                lambda: S.wgrad(x, a, None, ws), lambda: S.wgrad(x[:3], a, dw, ws),
+                lambda: S.wgrad(x, a, None, ws), lambda: S.wgrad(x, None, dw, ws), lambda: S.act_unpack(x, x), lambda: S.wgrad(x[:3], a, dw, ws),
                 lambda: S.wgrad(x, a, dw, ws.cpu()),
                 lambda: S.ActCheckpoint(a.codes[:, :32], a.scales, 64),
                 lambda: S.act_in(ws[1:], 4, 64)):
