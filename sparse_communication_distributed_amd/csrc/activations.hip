@@ -13,7 +13,7 @@ namespace {
 
 // ------------------------------------------------------------ pack, unpack
 
-// [16384][5632] bf16: pack 53-61 us, unpack 49 us, 280 MB each (4.6-5.7 TB/s).
+// [16384][5632] bf16: pack 50 us, unpack 46 us, 280 MB each (5.6-6.1 TB/s).
 //
 // A quad walks (row, block) pairs in row-major order, nquads at a time;
 // drow, dblk: nquads as rows and blocks, so that the walk needs no division.
@@ -166,7 +166,7 @@ __device__ __forceinline__ float norm_rstd(double sum, int64_t cols, float eps) 
 
 // Rows held in registers: T threads a row, C chunks of 8 columns a thread
 // (T * C * 8 >= cols).  Bound by memory: [16384][2048] bf16 with residual, h,
-// y and codes 57 us, 303 MB (5.3 TB/s); [8192][1280] 24 us (3.9 TB/s).
+// y and codes 58 us, 303 MB (5.2 TB/s); [8192][1280] 23 us (4.1 TB/s).
 constexpr int group_of(int T) { return T == 64 ? kThreads : T; }  // threads of a workgroup
 template <int DT, int T, int C, bool WHOLE>
 __global__ void __launch_bounds__(group_of(T)) norm_kernel(NormArgs a) {
@@ -286,8 +286,8 @@ struct BackRow {
 
 // Backward: dh, and the block's part of dweight in registers over its rows
 // (no atomics, so the order of the sum is fixed).  Bound by memory:
-// [16384][2048] bf16 with dres 48-50 us, 236 MB (4.8 TB/s); [8192][1280] 18.5 us
-// (4.0 TB/s).  Two rows at a time took 66 us instead of 47.
+// [16384][2048] bf16 with dres 44 us, 236 MB (5.4 TB/s); [8192][1280] 18 us (4.1
+// TB/s).  Two rows at a time took 66 us where one took 47.
 //
 // T threads a row, C chunks of 8 columns a thread.  With one chunk the next
 // row is loaded while this one is computed (more would not fit the
