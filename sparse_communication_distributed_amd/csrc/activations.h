@@ -43,15 +43,25 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 // 16 bytes at an element type's own alignment (gfx950 takes unaligned global
-// accesses), past the caches' retention: these matrices are read once.  With
-// ordinary loads [16384][5632] bf16 packed in 61 us instead of 50, and the
-// norm's backward pass of [16384][2048] took 49 us instead of 44 (its forward
-// pass 57.5 instead of 59.5).
+// accesses); STREAM: past the caches' retention.
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
-__device__ __forceinline__ void stream16(void* dst, const void* p) {
-  const u32x4 v = __builtin_nontemporal_load(static_cast<const u32x4_any*>(p));
+template <bool STREAM>
+__device__ __forceinline__ void load16(void* dst, const void* p) {
+  const u32x4_any* q = static_cast<const u32x4_any*>(p);
+  const u32x4 v = STREAM ? __builtin_nontemporal_load(q) : *q;
   __builtin_memcpy(dst, &v, 16);
 }
+
+// Matrices of 16-bit types are read with STREAM where a call touches more
+// bytes than the caches (256 MB) will hold next to what else runs.  Repeated
+// calls, ordinary against streaming loads, bf16: the norm of [16384][4096]
+// (320 MiB) 69 us against 64, its backward pass 72 against 67, and the backward
+// pass with dres of [16384][2048] (224 MiB) after its forward pass 49 against
+// 44; but pack of [16384][4096] (198 MiB) 30 against 35.5 and of [4096][2048]
+// 6.0 against 6.8, whose matrices the caches still hold.  fp32 gains nothing
+// (norm of [8192][4096] 58 us either way) and loses in the backward pass (73
+// against 78).
+constexpr int64_t kStreamBytes = int64_t(208) << 20;
 
 // 8 consecutive elements of a row as fp32, and back (rounded to nearest
 // even), as one or two 16-byte accesses.
@@ -61,10 +71,11 @@ struct Elem;
 template <>
 struct Elem<SCAPE_F32> {
   typedef float T;
+  template <bool STREAM>
   static __device__ __forceinline__ void load(const void* p, int64_t i, float (&v)[8]) {
     const float* q = static_cast<const float*>(p) + i;
-    __builtin_memcpy(&v[0], q, 16);
-    __builtin_memcpy(&v[4], q + 4, 16);
+    load16<STREAM>(&v[0], q);
+    load16<STREAM>(&v[4], q + 4);
   }
   static __device__ __forceinline__ void store(void* p, int64_t i, const float (&v)[8]) {
     float* q = static_cast<float*>(p) + i;
@@ -78,9 +89,10 @@ struct Elem<SCAPE_F32> {
 template <>
 struct Elem<SCAPE_BF16> {
   typedef uint16_t T;
+  template <bool STREAM>
   static __device__ __forceinline__ void load(const void* p, int64_t i, float (&v)[8]) {
     uint32_t u[4];
-    stream16(u, static_cast<const uint16_t*>(p) + i);
+    load16<STREAM>(u, static_cast<const uint16_t*>(p) + i);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       v[2 * j] = __uint_as_float(u[j] << 16);
@@ -102,9 +114,10 @@ struct Elem<SCAPE_BF16> {
 template <>
 struct Elem<SCAPE_F16> {
   typedef uint16_t T;
+  template <bool STREAM>
   static __device__ __forceinline__ void load(const void* p, int64_t i, float (&v)[8]) {
     _Float16 u[8];
-    stream16(u, static_cast<const uint16_t*>(p) + i);
+    load16<STREAM>(u, static_cast<const uint16_t*>(p) + i);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = (float)u[j];
   }
@@ -125,15 +138,15 @@ struct Elem<SCAPE_F16> {
 // The same 8 elements as they lie in memory, for loads that are kept under
 // way while something else is computed.  With WHOLE a chunk past the row is
 // the row's last one.
-template <int DT, bool WHOLE>
+template <int DT, bool WHOLE, bool STREAM>
 struct Raw8 {
   static constexpr int kWords = DT == SCAPE_F32 ? 8 : 4;
   uint32_t u[kWords];
   __device__ __forceinline__ void load(const void* p, int64_t row0, int64_t c, int64_t cols) {
     const char* q = static_cast<const char*>(p) + (row0 + (!WHOLE || c < cols ? c : cols - 8)) * (kWords / 2);
     if (WHOLE || c + 8 <= cols) {
-      stream16(u, q);
-      if (kWords == 8) stream16(u + kWords / 2, q + 16);
+      load16<STREAM>(u, q);
+      if (kWords == 8) load16<STREAM>(u + kWords / 2, q + 16);
     } else {
 #pragma unroll
       for (int j = 0; j < kWords; ++j) u[j] = 0;
@@ -168,14 +181,14 @@ struct Raw8 {
 // cols is a multiple of 8, so a chunk is all there or not at all, and one
 // past the row is loaded from the row's end and set to zero: no branch, behind
 // which the compiler would wait for every load under way.
-template <int DT, bool WHOLE = false>
+template <int DT, bool WHOLE = false, bool STREAM = false>
 __device__ __forceinline__ void load8(const void* p, int64_t row0, int64_t c, int64_t cols, float (&v)[8]) {
   if (WHOLE) {
-    Elem<DT>::load(p, row0 + (c < cols ? c : cols - 8), v);
+    Elem<DT>::template load<STREAM>(p, row0 + (c < cols ? c : cols - 8), v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = c < cols ? v[j] : 0.0f;
   } else if (c + 8 <= cols) {
-    Elem<DT>::load(p, row0 + c, v);
+    Elem<DT>::template load<STREAM>(p, row0 + c, v);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? Elem<DT>::get(p, row0 + c + j) : 0.0f;

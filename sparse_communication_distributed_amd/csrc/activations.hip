@@ -31,7 +31,7 @@ struct BlockWalk {
   }
 };
 
-template <int DT>
+template <int DT, bool STREAM>
 __global__ void __launch_bounds__(kThreads)
 pack_kernel(const void* __restrict__ x, int64_t ld, int64_t rows, int64_t cols, int64_t nblk, int64_t drow,
             int64_t dblk, int8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
@@ -40,7 +40,7 @@ pack_kernel(const void* __restrict__ x, int64_t ld, int64_t rows, int64_t cols, 
   for (BlockWalk w(tid >> 2, nblk); w.row < rows; w.next(drow, dblk, nblk)) {
     const int64_t c = w.blk * kActBlock + sub * 8;
     float v[8];
-    load8<DT>(x, w.row * ld, c, cols, v);
+    load8<DT, false, STREAM>(x, w.row * ld, c, cols, v);
     const uint32_t amax = quad_max(act_amax8(v));
     uint32_t s;
     const u32x2 q = act_encode(v, amax, &s);
@@ -73,6 +73,11 @@ unpack_kernel(const int8_t* __restrict__ codes, const uint8_t* __restrict__ scal
     }
     store8<DT>(out, w.row * ld, c, cols, v);
   }
+}
+
+// Whether a call that touches this many matrices, and codes, streams.
+bool streams(int dt, int matrices, const int8_t* codes, int64_t rows, int64_t cols) {
+  return dt != SCAPE_F32 && rows * cols > kStreamBytes / (matrices * (int64_t)dtype_bytes(dt) + (codes ? 1 : 0));
 }
 
 unsigned walk_grid(int64_t rows, int64_t nblk) {
@@ -120,12 +125,12 @@ struct NormArgs {
   float* rstd;
 };
 
-template <int DT, bool WHOLE = false>
+template <int DT, bool WHOLE = false, bool STREAM = false>
 __device__ __forceinline__ void load_sum(const NormArgs& a, int64_t row, int64_t c, float (&v)[8]) {
-  load8<DT, WHOLE>(a.x, row * a.x_ld, c, a.cols, v);
+  load8<DT, WHOLE, STREAM>(a.x, row * a.x_ld, c, a.cols, v);
   if (a.res) {
     float r[8];
-    load8<DT, WHOLE>(a.res, row * a.res_ld, c, a.cols, r);
+    load8<DT, WHOLE, STREAM>(a.res, row * a.res_ld, c, a.cols, r);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += r[j];
   }
@@ -166,9 +171,9 @@ __device__ __forceinline__ float norm_rstd(double sum, int64_t cols, float eps) 
 
 // Rows held in registers: T threads a row, C chunks of 8 columns a thread
 // (T * C * 8 >= cols).  Bound by memory: [16384][2048] bf16 with residual, h,
-// y and codes 58 us, 303 MB (5.2 TB/s); [8192][1280] 23 us (4.1 TB/s).
+// y and codes 57 us, 303 MB (5.3 TB/s); [8192][1280] 24 us (3.9 TB/s).
 constexpr int group_of(int T) { return T == 64 ? kThreads : T; }  // threads of a workgroup
-template <int DT, int T, int C, bool WHOLE>
+template <int DT, int T, int C, bool WHOLE, bool STREAM>
 __global__ void __launch_bounds__(group_of(T)) norm_kernel(NormArgs a) {
   __shared__ double lds[group_of(T) / 64];
   constexpr int kRows = group_of(T) / T;
@@ -178,7 +183,7 @@ __global__ void __launch_bounds__(group_of(T)) norm_kernel(NormArgs a) {
     double s = 0.0;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      load_sum<DT, WHOLE>(a, row, (int64_t)(i * T + t) * 8, v[i]);
+      load_sum<DT, WHOLE, STREAM>(a, row, (int64_t)(i * T + t) * 8, v[i]);
     }
 #pragma unroll
     for (int i = 0; i < C; ++i)
@@ -262,9 +267,9 @@ __device__ __forceinline__ void back_emit(const NormBackArgs& a, int64_t row, in
 }
 
 // One row's inputs of a thread, as they lie in memory.
-template <int DT, int C, bool WHOLE>
+template <int DT, int C, bool WHOLE, bool STREAM>
 struct BackRow {
-  Raw8<DT, WHOLE> dy[C], dres[C];
+  Raw8<DT, WHOLE, STREAM> dy[C], dres[C];
   u32x2 codes[C];
   uint32_t scale[C];
   float rstd;
@@ -286,14 +291,14 @@ struct BackRow {
 
 // Backward: dh, and the block's part of dweight in registers over its rows
 // (no atomics, so the order of the sum is fixed).  Bound by memory:
-// [16384][2048] bf16 with dres 44 us, 236 MB (5.4 TB/s); [8192][1280] 18 us (4.1
+// [16384][2048] bf16 with dres 44 us, 236 MB (5.4 TB/s); [8192][1280] 18.5 us (4.0
 // TB/s).  Two rows at a time took 66 us where one took 47.
 //
 // T threads a row, C chunks of 8 columns a thread.  With one chunk the next
 // row is loaded while this one is computed (more would not fit the
 // registers of enough waves).  With dh in dy's or dres's place a row is read
 // whole before any of it is written, and no other thread reads it.
-template <int DT, int T, int C, bool WHOLE>
+template <int DT, int T, int C, bool WHOLE, bool STREAM>
 __global__ void __launch_bounds__(group_of(T)) norm_back_kernel(NormBackArgs a) {
   __shared__ float lds[group_of(T) / 64];
   __shared__ float part[T == 64 ? 64 * C * 8 : 1];
@@ -309,11 +314,11 @@ __global__ void __launch_bounds__(group_of(T)) norm_back_kernel(NormBackArgs a) 
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
   }
   int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / T;
-  BackRow<DT, C, WHOLE> next;
+  BackRow<DT, C, WHOLE, STREAM> next;
   if (kAhead && row < a.rows) next.template load<T>(a, row, t);
   for (; row < a.rows; row += step) {
     if (!kAhead) next.template load<T>(a, row, t);
-    const BackRow<DT, C, WHOLE> cur = next;
+    const BackRow<DT, C, WHOLE, STREAM> cur = next;
     if (kAhead) next.template load<T>(a, row + step < a.rows ? row + step : row, t);
     float sum = 0.0f;
 #pragma unroll
@@ -490,10 +495,12 @@ void norm_launch(const NormArgs& a, hipStream_t s) {
   for_row_shape(a.cols, [&](auto t, auto c) {
     constexpr int T = decltype(t)::value, C = decltype(c)::value, per = group_of(T) / T;
     const unsigned grid = cap_grid((a.rows + per - 1) / per, 65536);
-    if (a.cols % 8 == 0)
-      norm_kernel<DT, T, C, true><<<grid, group_of(T), 0, s>>>(a);
+    if (a.cols % 8 != 0)
+      norm_kernel<DT, T, C, false, false><<<grid, group_of(T), 0, s>>>(a);
+    else if (streams(DT, 1 + (a.res != nullptr) + (a.h != nullptr) + (a.y != nullptr), a.codes, a.rows, a.cols))
+      norm_kernel<DT, T, C, true, DT != SCAPE_F32><<<grid, group_of(T), 0, s>>>(a);
     else
-      norm_kernel<DT, T, C, false><<<grid, group_of(T), 0, s>>>(a);
+      norm_kernel<DT, T, C, true, false><<<grid, group_of(T), 0, s>>>(a);
   });
 }
 
@@ -507,10 +514,12 @@ void back_launch(const NormBackArgs& a, unsigned parts, hipStream_t s) {
   }
   for_row_shape(a.cols, [&](auto t, auto c) {
     constexpr int T = decltype(t)::value, C = decltype(c)::value;
-    if (a.cols % 8 == 0)
-      norm_back_kernel<DT, T, C, true><<<parts, group_of(T), 0, s>>>(a);
+    if (a.cols % 8 != 0)
+      norm_back_kernel<DT, T, C, false, false><<<parts, group_of(T), 0, s>>>(a);
+    else if (streams(DT, 1 + (a.dres != nullptr) + (a.dh != nullptr), a.codes, a.rows, a.cols))
+      norm_back_kernel<DT, T, C, true, DT != SCAPE_F32><<<parts, group_of(T), 0, s>>>(a);
     else
-      norm_back_kernel<DT, T, C, false><<<parts, group_of(T), 0, s>>>(a);
+      norm_back_kernel<DT, T, C, true, false><<<parts, group_of(T), 0, s>>>(a);
   });
 }
 
@@ -523,8 +532,14 @@ hipError_t launch_act_pack(int64_t rows, int64_t cols, const scape_matrix& x, co
   const unsigned grid = walk_grid(rows, nblk);
   const int64_t quads = (int64_t)grid * kThreads / 4;
   const int64_t drow = quads / nblk, dblk = quads % nblk;
+  const bool stream = streams(x.dtype, 1, out.codes, rows, cols);
 #define PACK(DT) \
-  case DT: pack_kernel<DT><<<grid, kThreads, 0, s>>>(x.data, x.ld, rows, cols, nblk, drow, dblk, out.codes, out.scales); break;
+  case DT: \
+    if (stream) \
+      pack_kernel<DT, DT != SCAPE_F32><<<grid, kThreads, 0, s>>>(x.data, x.ld, rows, cols, nblk, drow, dblk, out.codes, out.scales); \
+    else \
+      pack_kernel<DT, false><<<grid, kThreads, 0, s>>>(x.data, x.ld, rows, cols, nblk, drow, dblk, out.codes, out.scales); \
+    break;
   switch (x.dtype) { PACK(SCAPE_F32) PACK(SCAPE_BF16) PACK(SCAPE_F16) }
 #undef PACK
   return hipGetLastError();

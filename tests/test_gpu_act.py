@@ -691,3 +691,42 @@ def test_gradient_rows_into_the_optimizer_step(S):
     torch.cuda.synchronize()
     for name, want in (("params", ora.gather("w")), ("m", ora.gather("m")), ("e", ora.gather("e"))):
         assert np.array_equal(getattr(opt, name).cpu().numpy().view(np.uint32), want.view(np.uint32)), name
+
+
+# ------------------------------------- matrices larger than the caches
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("cols", [2048, 2041])
+def test_large_matrices_like_their_parts(S, cols, dt):
+    """Calls on more bytes than the caches hold load otherwise; their rows
+    equal those of calls on an eighth of the rows, bit for bit."""
+    t, rows, n = DT[dt], 36264, 8
+    g = torch.Generator(DEV).manual_seed(21)
+    x, r = (torch.randn(rows, cols, device=DEV, generator=g).to(t) for _ in range(2))
+    w = torch.randn(cols, device=DEV, generator=g)
+    p, a = S.act_alloc(rows, cols, DEV), S.act_alloc(rows, cols, DEV)
+    y, h, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(rows, device=DEV)
+    dh, dw, dws = torch.empty_like(x), torch.empty(cols, device=DEV), torch.zeros(cols, device=DEV)
+    ws = torch.empty(S.rmsnorm_workspace_bytes(rows, cols), dtype=torch.uint8, device=DEV)
+    S.act_pack(x, p)
+    S.rmsnorm_pack(x, w, EPS, y, xhat=a, rstd=rstd, residual=r, h=h)
+    S.rmsnorm_backward(x, a, rstd, w, dh, dw, ws, dres=r)
+    m = rows // n
+    q, b = S.act_alloc(m, cols, DEV), S.act_alloc(m, cols, DEV)
+    y2, h2, rstd2, dh2 = (torch.empty_like(v[:m]) for v in (y, h, rstd, dh))
+    size = torch.zeros(cols, dtype=torch.float64, device=DEV)
+    for i in range(n):
+        s = slice(i * m, (i + 1) * m)
+        S.act_pack(x[s], q)
+        assert torch.equal(q.codes, p.codes[s]) and torch.equal(q.scales, p.scales[s])
+        S.rmsnorm_pack(x[s], w, EPS, y2, xhat=b, rstd=rstd2, residual=r[s], h=h2)
+        assert torch.equal(y2, y[s]) and torch.equal(h2, h[s]) and torch.equal(rstd2, rstd[s])
+        assert torch.equal(b.codes, a.codes[s]) and torch.equal(b.scales, a.scales[s])
+        S.rmsnorm_backward(x[s], b, rstd2, w, dh2, dws, ws, dres=r[s], accumulate=True)
+        assert torch.equal(dh2, dh[s])
+        xh = torch.empty(m, cols, device=DEV)
+        S.act_unpack(b, xh)
+        size += (x[s].double() * xh.double()).abs().sum(0)
+    # either sum rounds at most 36 times in a block's rows (rows / 1024), 16
+    # in a group of parts, 64 for the groups, and 8 between the calls
+    assert ((dw.double() - dws.double()).abs() <= 2 * 124 * U * (1 + 1e-4) * size).all()
