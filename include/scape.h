@@ -523,9 +523,10 @@ size_t scape_wgrad_workspace_bytes(int64_t rows, int64_t in, int64_t out, scape_
  * added to what dw and dbias hold if accumulate is not 0.  gain null: 1.
  * dbias null: left out.  dw is contiguous.  Products are exact and sums are
  * fp32: dy of fp32 is split into 3 bf16 terms that add up to it (below 2^-110
- * a term may be lost), dy of fp16 is multiplied in fp16 by the checkpoint
- * scaled to that type's range, in which values of the checkpoint are rounded
- * only where their scale lies more than 2^32 below the checkpoint's largest.
+ * a term may be lost), dy of fp16 is multiplied in fp16 by the checkpoint, each
+ * 32 columns of it scaled to that type's range, in which values are rounded
+ * only where their scale lies more than 2^32 below those columns' largest (by
+ * at most 2^-38 of the largest value there).
  */
 scape_status scape_wgrad(int64_t rows, int64_t in, int64_t out, scape_matrix dy, scape_act_view x, const float* gain,
                          float* dw, float* dbias, int32_t accumulate, void* workspace, size_t workspace_bytes,

@@ -9,13 +9,14 @@
 // sum, and what lies below its last place is lost (999 rows, 777 -> 1531: off
 // by 0.9e-7 of the norm, the bias by 0.6e-7; largest first 2.4e-7 and 2.9e-7).
 //
-// An fp16 dy is multiplied in fp16 (two bf16 terms took twice the time).  The
-// checkpoint is then scaled by a power of two that brings its largest scale
-// to 2^8 (127 * 2^8 is in range), and the sums are scaled back: its values
-// are exact in fp16 down to 2^-32 times that scale, and smaller ones round
-// to multiples of 2^-24 before scaling back.
+// An fp16 dy is multiplied in fp16 (two bf16 terms took twice the time).  Each
+// 32 columns of the checkpoint are then scaled by a power of two that brings
+// their largest scale to 2^8 (127 * 2^8 is in range), and their sums are scaled
+// back: values are exact in fp16 down to 2^-32 times that scale, and smaller
+// ones round to multiples of 2^-24 before scaling back, by at most 2^-38 of the
+// largest value of those columns.
 //
-// Launches: for fp16 the largest scale; prepare (the checkpoint in 16 bits,
+// Launches: for fp16 the largest scales; prepare (the checkpoint in 16 bits,
 // and dy's terms where dy cannot be read as it lies); the product over row
 // splits; with more than one split the join of their partial sums.
 
@@ -38,35 +39,56 @@ int64_t ceil_div(int64_t x, int64_t t) { return (x + t - 1) / t; }
 
 // ------------------------------------------------------------------ prepare
 
-// The largest finite scale byte, as kMaxParts partial maxima.
+constexpr int kTopExp = 8;  // fp16: the largest scale of 32 columns becomes 2^kTopExp
+
+// The scales [rows][nblk] as a matrix of rows of `flat` columns: rows of fewer
+// than 64 scales are joined in whole numbers up to 64, so that narrow matrices
+// occupy the threads, too.  pitch: flat up to whole slabs of 64.
+struct Flat {
+  int64_t nblk, flat, pitch;
+  explicit Flat(int64_t n) : nblk(n), flat(n < 64 ? 64 / n * n : n), pitch((flat + 63) / 64 * 64) {}
+  int64_t rows(int64_t scales) const { return (scales + flat - 1) / flat; }
+};
+
+// parts[blockIdx.y][flat column] = the largest finite scale byte of its block of
+// columns over one in gridDim.y of the groups of 64 flat rows.  A thread takes
+// 16 columns of a row.
 constexpr int kMaxParts = 64;
-constexpr int kTopExp = 8;  // the largest scale becomes 2^kTopExp in fp16
-__global__ void __launch_bounds__(1024)
-scale_max_kernel(const uint8_t* __restrict__ scales, int64_t n, uint32_t* __restrict__ parts) {
-  __shared__ uint32_t lds[16];
-  uint32_t m = 0;
-  const int64_t step = (int64_t)kMaxParts * 1024 * 16;
-  for (int64_t i = ((int64_t)blockIdx.x * 1024 + threadIdx.x) * 16; i < n; i += step) {
+__global__ void __launch_bounds__(kThreads)
+scale_max_kernel(const uint8_t* __restrict__ scales, int64_t n, int64_t nblk, int64_t flat, int64_t pitch,
+                 uint8_t* __restrict__ parts) {
+  static_assert(kThreads == 256, "64 rows of 4 threads");
+  __shared__ __attribute__((aligned(16))) uint8_t rows[64][64], quarters[4][64];
+  const int64_t col = (int64_t)blockIdx.x * 64 + (threadIdx.x & 3) * 16;
+  uint8_t m[16] = {};
+  for (int64_t r = (int64_t)blockIdx.y * 64 + (threadIdx.x >> 2); r * flat < n; r += (int64_t)gridDim.y * 64) {
+    const int64_t i = r * flat + col, left = flat - col < n - i ? flat - col : n - i;
     uint8_t b[16];
-    if (i + 16 <= n) {
+    if (left >= 16) {
       __builtin_memcpy(b, scales + i, 16);
     } else {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) b[j] = i + j < n ? scales[i + j] : 0;
+      for (int j = 0; j < 16; ++j) b[j] = j < left ? scales[i + j] : 0;
     }
 #pragma unroll
-    for (int j = 0; j < 16; ++j) m = b[j] != 255 && b[j] > m ? b[j] : m;
+    for (int j = 0; j < 16; ++j) m[j] = b[j] != 255 && b[j] > m[j] ? b[j] : m[j];
   }
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    const uint32_t o = __shfl_xor(m, d, 64);
-    m = o > m ? o : m;
-  }
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = m;
+  __builtin_memcpy(&rows[threadIdx.x >> 2][(threadIdx.x & 3) * 16], m, 16);
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < 16; ++w) m = lds[w] > m ? lds[w] : m;
-    parts[blockIdx.x] = m;
+  const int c = threadIdx.x & 63, g = threadIdx.x >> 6;
+  uint8_t t = 0;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) t = rows[g * 16 + j][c] > t ? rows[g * 16 + j][c] : t;
+  quarters[g][c] = t;
+  __syncthreads();
+  if (g == 0) {
+    for (int j = 1; j < 4; ++j) t = quarters[j][c] > t ? quarters[j][c] : t;
+    // joined rows (flat <= 64): the columns nblk apart, 2, 4, 8 .. of them
+    for (int d = (int)nblk; d < (int)flat; d *= 2) {
+      const int o = __shfl((int)t, c + d < (int)flat ? c + d : c + d - (int)flat, 64);
+      t = o > t ? (uint8_t)o : t;
+    }
+    parts[blockIdx.y * pitch + (int64_t)blockIdx.x * 64 + c] = t;
   }
 }
 
@@ -75,8 +97,10 @@ struct PrepArgs {
   const int8_t* codes;
   const uint8_t* scales;
   uint16_t* x;  // [rows_pad][nblk * 32] bf16 (fp16 for an fp16 dy), zero past rows
-  const uint32_t* max_parts;  // fp16: the partial maxima of the scales
-  float* back;                // fp16: receives what the sums are multiplied by
+  const uint8_t* max_parts;  // fp16: partial maxima [n_parts][pitch] of the scales
+  int n_parts;
+  int64_t flat, pitch;  // fp16: those of Flat
+  float* back;          // fp16: [nblk], receives what each block's sums are multiplied by
   const void* dy;
   int64_t dy_ld;
   // dy's terms, smallest first, [terms][t_rows][out_pad] in 16 bits of rows t_first .., zero past
@@ -101,42 +125,67 @@ __device__ __forceinline__ uint32_t upper_halves(uint32_t a, uint32_t b) {
   return __builtin_amdgcn_perm(b, a, 0x07060302u);
 }
 
+// fp16: a workgroup takes one in (x_blocks / slabs) of the flat rows in a slab of
+// 64 flat columns, 4 threads a column, so that a thread's shift of the scale
+// byte is found once.
+__device__ __forceinline__ void prepare_x_f16(const PrepArgs& a) {
+  __shared__ __attribute__((aligned(16))) uint8_t parts[kMaxParts][64], quarters[4][64];
+  const int64_t slabs = a.pitch / 64, slab = blockIdx.x % slabs;
+  const int64_t first = blockIdx.x / slabs, step = a.x_blocks / slabs;
+  u32x4 p = {0, 0, 0, 0};
+  if ((int)(threadIdx.x >> 2) < a.n_parts)
+    __builtin_memcpy(&p, __builtin_assume_aligned(a.max_parts + (threadIdx.x >> 2) * a.pitch + slab * 64 + (threadIdx.x & 3) * 16, 16), 16);
+  __builtin_memcpy(&parts[threadIdx.x >> 2][(threadIdx.x & 3) * 16], &p, 16);
+  __syncthreads();
+  const int c = threadIdx.x & 63, g = threadIdx.x >> 6;
+  uint8_t t = 0;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) t = parts[g * 16 + j][c] > t ? parts[g * 16 + j][c] : t;
+  quarters[g][c] = t;
+  __syncthreads();
+  const int64_t col = slab * 64 + (threadIdx.x >> 2);
+  if (col >= a.flat) return;
+  int m = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m = quarters[j][col & 63] > m ? quarters[j][col & 63] : m;
+  const int shift = 127 + kTopExp - m;
+  if (first == 0 && col < a.nblk && (threadIdx.x & 3) == 0) a.back[col] = ldexpf(1.0f, -shift);
+  const int64_t full = a.rows * a.nblk, n = a.rows_pad * a.nblk;  // blocks
+  for (int64_t b = first * a.flat + col; b < n; b += step * a.flat) {
+    u32x4 o = {0, 0, 0, 0};
+    const int64_t i = b * 4 + (threadIdx.x & 3);
+    if (b < full) {
+      float v[8];
+      const uint32_t s = a.scales[b];
+      const int e = (int)s + shift;  // under 1: less than any fp16 number
+      act_decode(reinterpret_cast<const u32x2*>(a.codes)[i], s == 0 || s == 255 ? s : (e < 1 ? 0u : (uint32_t)e), v);
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+        o[h] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)v[2 * h], (_Float16)v[2 * h + 1]});
+    }
+    reinterpret_cast<u32x4*>(a.x)[i] = o;
+  }
+}
+
 // Bound by memory: [16384][2048] codes to bf16 18 us (102 MB, 5.6 TB/s).
 template <int DT>
 __global__ void __launch_bounds__(kThreads) wgrad_prepare_kernel(PrepArgs a) {
   if (blockIdx.x < a.x_blocks) {
-    const int64_t n = a.rows_pad * a.nblk * 4, step = (int64_t)a.x_blocks * kThreads;
-    const int64_t full = a.rows * a.nblk * 4;
-    int shift = 0;  // of the scale byte
-    if (DT == SCAPE_F16) {
-      uint32_t m = a.max_parts[threadIdx.x & (kMaxParts - 1)];
-#pragma unroll
-      for (int d = 32; d >= 1; d >>= 1) {
-        const uint32_t o = __shfl_xor(m, d, 64);
-        m = o > m ? o : m;
-      }
-      shift = 127 + kTopExp - (int)m;
-      if (blockIdx.x == 0 && threadIdx.x == 0) *a.back = ldexpf(1.0f, -shift);
-    }
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
-      u32x4 p = {0, 0, 0, 0};
-      if (i < full) {
-        float v[8];
-        const u32x2 q = reinterpret_cast<const u32x2*>(a.codes)[i];
-        const uint32_t s = a.scales[i >> 2];
-        if (DT == SCAPE_F16) {
-          const int e = (int)s + shift;  // under 1: less than any fp16 number
-          act_decode(q, s == 0 || s == 255 ? s : (e < 1 ? 0u : (uint32_t)e), v);
-#pragma unroll
-          for (int h = 0; h < 4; ++h)
-            p[h] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)v[2 * h], (_Float16)v[2 * h + 1]});
-        } else {
-          act_decode(q, s, v);
+    if constexpr (DT == SCAPE_F16) {
+      prepare_x_f16(a);
+    } else {
+      const int64_t n = a.rows_pad * a.nblk * 4, step = (int64_t)a.x_blocks * kThreads;
+      const int64_t full = a.rows * a.nblk * 4;
+      for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
+        u32x4 p = {0, 0, 0, 0};
+        if (i < full) {
+          float v[8];
+          act_decode(reinterpret_cast<const u32x2*>(a.codes)[i], a.scales[i >> 2], v);
 #pragma unroll
           for (int h = 0; h < 4; ++h) p[h] = upper_halves(__float_as_uint(v[2 * h]), __float_as_uint(v[2 * h + 1]));
         }
+        reinterpret_cast<u32x4*>(a.x)[i] = p;
       }
-      reinterpret_cast<u32x4*>(a.x)[i] = p;
     }
     return;
   }
@@ -176,8 +225,8 @@ struct WgradArgs {
   int64_t tail_step;
   const char* b;         // the checkpoint in 16 bits, zero past rows to a whole stage
   int64_t b_step, b_cols;
-  const float* back;     // fp16: the sums' scale.  It and gain are applied here
-  const float* gain;     // only when there is one split
+  const float* back;     // fp16: the sums' scale for each 32 columns.  It and gain
+  const float* gain;     // are applied here only when there is one split
   float* dw;             // [splits][out][in], or dw itself (one split)
   float* db;             // [splits][out], or dbias itself; null: none
   bool accumulate;       // one split
@@ -424,7 +473,6 @@ __global__ void __launch_bounds__(kWaves * 64) wgrad_kernel(WgradArgs a) {
 
   // Element e of a 32x32 accumulator: row 8*(e/4) + 4*(lane/32) + e%4, column
   // lane%32.  The address is a uniform row start and the lane's offset.
-  const float back = F16 && a.back ? *a.back : 1.0f;
   const int64_t m_first = m0 + wm, n_first = n0 + wn;
   const uint32_t lane_off = (uint32_t)(4 * (lane >> 5) * a.in + (lane & 31));
   const int64_t rows_left = a.out - m_first - 4 * (lane >> 5), cols_left = a.in - n_first - (lane & 31);
@@ -433,6 +481,7 @@ __global__ void __launch_bounds__(kWaves * 64) wgrad_kernel(WgradArgs a) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
       const bool col = whole.value || j * 32 < cols_left;
+      const float back = F16 && a.back && n_first + j * 32 < a.in ? a.back[(n_first >> 5) + j] : 1.0f;
       const float g = a.gain && col ? (a.gain + n_first + j * 32)[lane & 31] : 1.0f;
 #pragma unroll
       for (int i = 0; i < FM; ++i)
@@ -468,8 +517,8 @@ __global__ void __launch_bounds__(kWaves * 64) wgrad_kernel(WgradArgs a) {
 
 // --------------------------------------------------------------------- join
 
-// out[i] (+)= gain[i % in] * back * (the sum of the splits' partial sums, in
-// order), and for the bias behind them the plain sum.  VEC: 4 elements a
+// out[i] (+)= gain[i % in] * back[i % in / 32] * (the sum of the splits' partial
+// sums, in order), and for the bias behind them the plain sum.  VEC: 4 elements a
 // thread (in % 4 == 0, out 16-byte aligned).  5 splits of 1280 x 1280: 8.7 us
 // (39 MB, 4.5 TB/s).
 template <bool VEC>
@@ -479,7 +528,6 @@ join_kernel(const float* __restrict__ parts, int splits, int64_t n, int64_t in, 
             int64_t n_bias, float* __restrict__ bias, bool accumulate) {
   constexpr int V = VEC ? 4 : 1;
   const int64_t step = (int64_t)gridDim.x * kThreads, tid = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const float k = back ? *back : 1.0f;
   for (int64_t i = tid * V; i < n; i += step * V) {
     float s[V];
     __builtin_memcpy(s, __builtin_assume_aligned(parts + i, 4 * V), 4 * V);
@@ -489,7 +537,8 @@ join_kernel(const float* __restrict__ parts, int splits, int64_t n, int64_t in, 
 #pragma unroll
       for (int j = 0; j < V; ++j) s[j] += q[j];
     }
-    const int64_t c = !gain ? 0 : n < (int64_t(1) << 32) ? (int64_t)((uint32_t)i % (uint32_t)in) : i % in;
+    const int64_t c = !gain && !back ? 0 : n < (int64_t(1) << 32) ? (int64_t)((uint32_t)i % (uint32_t)in) : i % in;
+    const float k = back ? back[c / kActBlock] : 1.0f;
     float* o = out + i;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -570,7 +619,7 @@ struct Layout {  // of the workspace, in bytes
   bool as_it_lies;
   int terms;
   int64_t rows_pad, out_pad, t_first, t_rows;
-  size_t max, x, dy, parts, total;
+  size_t max, back, x, dy, parts, total;
 };
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -582,8 +631,13 @@ Layout layout_of(int64_t rows, int64_t in, int64_t out, const scape_matrix& dy, 
   l.out_pad = ceil_div(out, 8) * 8;
   l.t_first = l.as_it_lies ? rows / kBK * kBK : 0;
   l.t_rows = l.rows_pad - l.t_first;
-  l.max = 0;  // kMaxParts words, then the float `back`
-  l.x = 512;
+  l.max = 0;
+  l.back = l.x = 256;
+  if (dy.dtype == SCAPE_F16) {
+    const Flat f(act_blocks(in));
+    l.back = align256((size_t)(kMaxParts * f.pitch));
+    l.x = l.back + align256((size_t)f.nblk * 4);
+  }
   l.dy = l.x + align256((size_t)l.rows_pad * (size_t)act_pitch(in) * 2);
   l.parts = l.dy + align256((size_t)l.terms * (size_t)l.t_rows * (size_t)l.out_pad * 2);
   l.total = l.parts + (p.splits == 1 ? 0 : align256((size_t)p.splits * (size_t)out * (size_t)(in + 1) * 4));
@@ -620,20 +674,28 @@ hipError_t launch_wgrad(int64_t rows, int64_t in, int64_t out, const scape_matri
   const Plan plan = wgrad_plan(rows, in, out, terms_of(dy.dtype));
   const Layout l = layout_of(rows, in, out, dy, plan);
   char* const base = static_cast<char*>(ws);
-  uint32_t* const max_parts = reinterpret_cast<uint32_t*>(base + l.max);
-  float* const back = f16 && rows > 0 ? reinterpret_cast<float*>(max_parts + kMaxParts) : nullptr;
+  uint8_t* const max_parts = reinterpret_cast<uint8_t*>(base + l.max);
+  float* const back = f16 && rows > 0 ? reinterpret_cast<float*>(base + l.back) : nullptr;
   hipError_t e = hipSuccess;
   if (rows > 0) {
+    const Flat f(act_blocks(in));
+    const int64_t scales = rows * f.nblk, groups = ceil_div(f.rows(scales), 64);
+    const unsigned n_parts = (unsigned)(groups < kMaxParts ? groups : kMaxParts);
     if (f16) {
-      scale_max_kernel<<<kMaxParts, 1024, 0, s>>>(x.scales, rows * act_blocks(in), max_parts);
+      scale_max_kernel<<<dim3((unsigned)(f.pitch / 64), n_parts), kThreads, 0, s>>>(x.scales, scales, f.nblk, f.flat,
+                                                                                   f.pitch, max_parts);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    PrepArgs p{rows, l.rows_pad, act_blocks(in), out, l.out_pad, x.codes, x.scales,
-               reinterpret_cast<uint16_t*>(base + l.x), max_parts, back, dy.data, dy.ld,
+    PrepArgs p{rows, l.rows_pad, f.nblk, out, l.out_pad, x.codes, x.scales, reinterpret_cast<uint16_t*>(base + l.x),
+               max_parts, (int)n_parts, f.flat, f.pitch, back, dy.data, dy.ld,
                reinterpret_cast<uint16_t*>(base + l.dy), l.t_first, l.t_rows, 0};
     int64_t xb = ceil_div(l.rows_pad * p.nblk * 4, kThreads), db = ceil_div(l.t_rows * (l.out_pad / 8), kThreads);
     if (xb > 8192) xb = 8192;
     if (db > 8192) db = 8192;
+    if (f16) {  // every slab as many workgroups: at most its rows, and about 4096 in all
+      const int64_t slabs = f.pitch / 64, most = slabs < 4096 ? 4096 / slabs : 1, need = f.rows(l.rows_pad * f.nblk);
+      xb = slabs * (need < most ? need : most);
+    }
     p.x_blocks = (unsigned)xb;
     const unsigned grid = (unsigned)(xb + db);
     switch (dy.dtype) {
