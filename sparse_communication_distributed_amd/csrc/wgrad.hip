@@ -243,10 +243,18 @@ __device__ __forceinline__ void lds_barrier() {
 
 // 16 bytes a lane from memory to LDS without a register: lane l's go to
 // lds + 16 * l.  The address is base (the same for the wave) + off bytes.
-// The compiler does not count it: wait for it with wait_vm.
+// The compiler does not count it: wait for it with wait_vm.  m0 is the compiler's
+// own and declared as overwritten, so that it keeps no value there across this;
+// its warning that m0 is not restored says what is meant.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_to_lds(const void* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(lds), "v"(off), "s"(base) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(lds), "v"(off), "s"(base)
+               : "memory", "m0");
 }
+#pragma clang diagnostic pop
 // Waits until at most N of the wave's loads from memory are under way.
 template <int N>
 __device__ __forceinline__ void wait_vm() {
