@@ -427,9 +427,11 @@ scape_status scape_count_nonfinite(const float* x, int64_t count, uint64_t* nonf
  * The 32 columns of a block are q * 2^(s - 127), |q| <= 127, s the scale
  * byte.  s is the lowest >= 1 at which the block's largest magnitude is at
  * most 127 quanta, and q rounds to nearest (ties to even), so a value is off
- * by at most half a quantum, 1/127 of the block's largest magnitude (at the
- * largest scale 249 codes end at 63, so that no finite value becomes infinite,
- * and the error is at most 1.5 quanta).  s = 0:
+ * by at most half a quantum.  For 2 <= s <= 248 that is at most 1/127 of the
+ * block's largest magnitude.  At s = 1 it is 2^-127 whatever the magnitudes: a
+ * block of less than 63.5 * 2^-126 may lose more than 1/127, and one of at most
+ * 2^-127 all of it.  At the largest scale 249 codes end at 63, so that no
+ * finite value becomes infinite, and the error is at most 1.5 quanta.  s = 0:
  * all zero.  s = 255: the block held an infinity or a NaN, and all of it
  * reads back as NaN.  Every value has at most 8 significant bits and is
  * exact in bf16.
@@ -468,7 +470,7 @@ scape_status scape_act_slot(int64_t rows, int64_t cols, void* buffer, scape_act_
 scape_status scape_act_pack(int64_t rows, int64_t cols, scape_matrix x, scape_act_view out, hipStream_t stream);
 
 /* out = the values of a checkpoint, times gain[c] (fp32 [cols]) if gain is
- * not null, rounded to out's type (fp16 without a gain: +-65536, to which the
+ * not null (an fp32 product), rounded to out's type (fp16 without a gain: +-65536, to which the
  * values next to its largest round, reads as +-65504). */
 scape_status scape_act_unpack(int64_t rows, int64_t cols, scape_act_view a, const float* gain, scape_matrix out,
                               hipStream_t stream);

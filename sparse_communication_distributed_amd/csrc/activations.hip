@@ -162,9 +162,10 @@ __device__ __forceinline__ void norm_emit(const NormArgs& a, int64_t row, int64_
   }
 }
 
-// The reciprocal RMS.  Binary64, so that rstd (and with it every code, which
-// a last-bit change of rstd could move across a rounding border) does not
-// depend on how many threads share a row.
+// The reciprocal RMS.  The sum is binary64: how many threads share a row
+// changes its order, and with it the last bits of 53, which reach rstd's 24
+// practically never (a change of rstd's last bit could move codes across
+// rounding borders).  For one row width the order is fixed.
 __device__ __forceinline__ float norm_rstd(double sum, int64_t cols, float eps) {
   return (float)(1.0 / sqrt(sum / (double)cols + (double)eps));
 }

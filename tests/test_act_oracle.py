@@ -51,6 +51,28 @@ def test_error_is_at_most_half_a_quantum(seed):
     assert (np.abs(v - x) <= amax / 127.0).all()
 
 
+def test_error_bound_at_each_scale():
+    """Half a quantum at every scale but the largest; 1/127 of the block's
+    largest magnitude between the lowest scale and the largest."""
+    r = np.random.default_rng(9)
+    mant = r.uniform(1.0, 2.0, (256, 1))
+    for lo in (-149, -135, -128, -126, -121, -120, 0, 100, 127):
+        x = (r.uniform(-1.0, 1.0, (256, 32)) * mant * 2.0 ** lo).clip(-3.4e38, 3.4e38).astype(np.float32)
+        q, s = A.pack(x)
+        err = np.abs(A.unpack(q, s, 32) - x).max(axis=1)
+        amax = np.abs(x).max(axis=1).astype(np.float64)
+        quantum = np.ldexp(1.0, s[:, 0].astype(np.int64) - 127)
+        low, top = s[:, 0] <= 1, s[:, 0] == 249
+        assert (err[~top] <= quantum[~top] / 2).all() and (err[top] <= 1.5 * quantum[top]).all()
+        assert (err[~low & ~top] <= amax[~low & ~top] / 127.0).all()
+        assert (err[low] <= 2.0 ** -127).all()
+        if lo <= -128:  # the relative bound ends there: everything is lost
+            assert low.all() and (err == amax).all()
+    x = np.linspace(0, float(np.finfo(np.float32).max), 32, dtype=np.float64).astype(np.float32)[None]
+    q, s = A.pack(x)
+    assert s.tolist() == [[249]] and (np.abs(A.unpack(q, s, 32) - x) <= 1.5 * 2.0 ** 122).all()
+
+
 def test_values_are_exact_in_bf16():
     r = np.random.default_rng(3)
     q, s = A.pack((r.standard_normal((64, 64)) * 10.0 ** r.uniform(-30, 30, (64, 1))).astype(np.float32))
