@@ -516,6 +516,13 @@ scape_status scape_rmsnorm_backward(int64_t rows, int64_t cols, scape_matrix dy,
  * 0 if a size is invalid. */
 size_t scape_wgrad_workspace_bytes(int64_t rows, int64_t in, int64_t out, scape_matrix dy);
 
+/* How scape_wgrad divides its work for these sizes and a dy of this type (a
+ * scape_dtype), chosen by measured rates: a workgroup sums a tile of
+ * *tile_out x *tile_in elements of dw (either may be null) over one of the
+ * returned number of splits of the rows; with more than one, a further launch
+ * adds the splits' sums in order.  -1 if a size or the type is invalid. */
+int32_t scape_wgrad_splits(int64_t rows, int64_t in, int64_t out, int32_t dtype, int32_t* tile_out, int32_t* tile_in);
+
 /*
  * Gradient of a linear layer's weight [out][in] and bias [out] from the
  * checkpoint of its input x [rows][in] and the gradient dy [rows][out] of

@@ -147,6 +147,17 @@ scape_status scape_rmsnorm_backward(int64_t rows, int64_t cols, scape_matrix dy,
                    "rmsnorm backward");
 }
 
+int32_t scape_wgrad_splits(int64_t rows, int64_t in, int64_t out, int32_t dtype, int32_t* tile_out,
+                           int32_t* tile_in) {
+  if (!rows_ok(rows) || !cols_ok(in) || !cols_ok(out) || in * out > kMaxWeight) return -1;
+  if (dtype != SCAPE_F32 && dtype != SCAPE_BF16 && dtype != SCAPE_F16) return -1;
+  int m, n;
+  const int splits = wgrad_splits(rows, in, out, dtype, &m, &n);
+  if (tile_out) *tile_out = m;
+  if (tile_in) *tile_in = n;
+  return splits;
+}
+
 size_t scape_wgrad_workspace_bytes(int64_t rows, int64_t in, int64_t out, scape_matrix dy) {
   if (!rows_ok(rows) || !cols_ok(in) || !cols_ok(out) || in * out > kMaxWeight) return 0;
   return wgrad_workspace(rows, in, out, dy);

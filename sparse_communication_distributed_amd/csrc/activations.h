@@ -30,6 +30,8 @@ hipError_t launch_rmsnorm_backward(int64_t rows, int64_t cols, const scape_matri
 // Bytes of scratch of a weight gradient: the checkpoint as bf16, dy's terms
 // (those of every type's dy where dy.data is null), the splits' partial sums.
 size_t wgrad_workspace(int64_t rows, int64_t in, int64_t out, const scape_matrix& dy);
+// The number of splits of the rows, and the tile of dw.
+int wgrad_splits(int64_t rows, int64_t in, int64_t out, int dtype, int* tile_out, int* tile_in);
 hipError_t launch_wgrad(int64_t rows, int64_t in, int64_t out, const scape_matrix& dy, const scape_act_view& x,
                         const float* gain, float* dw, float* dbias, bool accumulate, void* ws, hipStream_t s);
 

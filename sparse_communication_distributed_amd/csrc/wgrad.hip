@@ -675,6 +675,13 @@ size_t wgrad_workspace(int64_t rows, int64_t in, int64_t out, const scape_matrix
   return most;
 }
 
+int wgrad_splits(int64_t rows, int64_t in, int64_t out, int dtype, int* tile_out, int* tile_in) {
+  const Plan p = wgrad_plan(rows, in, out, terms_of(dtype));
+  *tile_out = kShapes[p.shape].bm;
+  *tile_in = kShapes[p.shape].bn;
+  return p.splits;
+}
+
 hipError_t launch_wgrad(int64_t rows, int64_t in, int64_t out, const scape_matrix& dy, const scape_act_view& x,
                         const float* gain, float* dw, float* dbias, bool accumulate, void* ws, hipStream_t s) {
   if (rows < 1 && accumulate) return hipSuccess;

@@ -105,6 +105,8 @@ _SIGS = {
     "scape_rmsnorm_backward": (c_int, [c_int64, c_int64, Matrix, ActView, c_void_p, c_void_p, Matrix, Matrix,
                                        c_void_p, c_int32, c_void_p, c_size_t, c_void_p]),
     "scape_wgrad_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64, Matrix]),
+    "scape_wgrad_splits": (c_int32, [c_int64, c_int64, c_int64, c_int32, ctypes.POINTER(c_int32),
+                                     ctypes.POINTER(c_int32)]),
     "scape_wgrad": (c_int, [c_int64, c_int64, c_int64, Matrix, ActView, c_void_p, c_void_p, c_void_p, c_int32,
                             c_void_p, c_size_t, c_void_p]),
     "scape_status_string": (c_char_p, [c_int]),
@@ -509,20 +511,26 @@ _NO_ACT = ActView(None, None)
 _DTYPES = None
 
 
-def _matrix(t, name: str, rows: int, cols: int, device: int) -> Matrix:
-    """A [rows][cols] device tensor of fp32, bf16 or fp16 with consecutive
-    elements in a row and rows that do not overlap; None: no matrix."""
+def _dtype(t, name: str) -> int:
+    """The scape_dtype of a torch dtype."""
     global _DTYPES
-    if t is None:
-        return _NO_MATRIX
     if _DTYPES is None:
         import torch
         _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    dt = _DTYPES.get(t)
+    if dt is None:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16 (got {t})")
+    return dt
+
+
+def _matrix(t, name: str, rows: int, cols: int, device: int) -> Matrix:
+    """A [rows][cols] device tensor of fp32, bf16 or fp16 with consecutive
+    elements in a row and rows that do not overlap; None: no matrix."""
+    if t is None:
+        return _NO_MATRIX
     if t.get_device() != device:  # -1: host memory
         raise ValueError(f"{name} must be a tensor on device {device} (got {t.device})")
-    dt = _DTYPES.get(t.dtype)
-    if dt is None:
-        raise ValueError(f"{name} must be float32, bfloat16 or float16 (got {t.dtype})")
+    dt = _dtype(t.dtype, name)
     if t.shape != (rows, cols):
         raise ValueError(f"{name} must have shape ({rows}, {cols}) (got {tuple(t.shape)})")
     ld, one = t.stride()
@@ -657,6 +665,14 @@ def wgrad_workspace_bytes(rows: int, n_in: int, n_out: int, dy=None) -> int:
     """Bytes of workspace of wgrad with this dy [rows][out], or with any."""
     m = _NO_MATRIX if dy is None else _matrix(dy, "dy", rows, n_out, _device_of(dy, "dy"))
     return int(lib().scape_wgrad_workspace_bytes(rows, n_in, n_out, m))
+
+
+def wgrad_splits(rows: int, n_in: int, n_out: int, dtype):
+    """(splits, tile_out, tile_in): how wgrad divides its work for a dy of
+    this torch dtype (splits -1: invalid size)."""
+    m, n = c_int32(), c_int32()
+    splits = lib().scape_wgrad_splits(rows, n_in, n_out, _dtype(dtype, "dtype"), ctypes.byref(m), ctypes.byref(n))
+    return int(splits), m.value, n.value
 
 
 def wgrad(dy, x: ActCheckpoint, dw, workspace, gain=None, dbias=None, accumulate: bool = False, stream=None) -> None:
