@@ -459,6 +459,9 @@ class ActCheckpoint:
 
     def __init__(self, codes, scales, cols: int):
         import torch
+        for t, name in ((codes, "codes"), (scales, "scales")):
+            if not torch.is_tensor(t):
+                raise _no_tensor(t, name)
         self.codes, self.scales, self.cols = codes, scales, int(cols)
         nb = (self.cols + ACT_BLOCK - 1) // ACT_BLOCK
         if codes.dim() != 2 or scales.dim() != 2 or codes.dtype != torch.int8 or scales.dtype != torch.uint8:
@@ -506,6 +509,10 @@ def act_alloc(rows: int, cols: int, device) -> ActCheckpoint:
     return act_in(torch.empty(need, dtype=torch.uint8, device=device), rows, cols)
 
 
+def _no_tensor(t, name: str) -> ValueError:
+    return ValueError(f"{name} must be a tensor (got {type(t).__name__})")
+
+
 _NO_MATRIX = Matrix(None, 0, 0)
 _NO_ACT = ActView(None, None)
 _DTYPES = None
@@ -528,7 +535,11 @@ def _matrix(t, name: str, rows: int, cols: int, device: int) -> Matrix:
     elements in a row and rows that do not overlap; None: no matrix."""
     if t is None:
         return _NO_MATRIX
-    if t.get_device() != device:  # -1: host memory
+    try:
+        at = t.get_device()  # -1: host memory
+    except AttributeError:
+        raise _no_tensor(t, name) from None
+    if at != device:
         raise ValueError(f"{name} must be a tensor on device {device} (got {t.device})")
     dt = _dtype(t.dtype, name)
     if t.shape != (rows, cols):
@@ -547,8 +558,12 @@ def _vector(t, name: str, numel: int, device: int) -> Optional[int]:
     """Address of a contiguous fp32 device tensor of `numel` elements."""
     if t is None:
         return None
+    try:
+        at = t.get_device()
+    except AttributeError:
+        raise _no_tensor(t, name) from None
     import torch
-    if t.get_device() != device or t.dtype != torch.float32:
+    if at != device or t.dtype != torch.float32:
         raise ValueError(f"{name} must be a float32 tensor on device {device} (got {t.dtype} on {t.device})")
     if not t.is_contiguous() or t.numel() != numel:
         raise ValueError(f"{name} must be contiguous with {numel} elements (got {tuple(t.shape)})")
@@ -572,7 +587,11 @@ def _act(a, name: str, rows: int, cols: int, device: int) -> ActView:
 
 
 def _workspace(t, need: int, device: int):
-    if t.get_device() != device or not t.is_contiguous():
+    try:
+        at = t.get_device()
+    except AttributeError:
+        raise _no_tensor(t, "workspace") from None
+    if at != device or not t.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on device {device}")
     have = t.numel() * t.element_size()
     if have < need:
@@ -583,7 +602,11 @@ def _workspace(t, need: int, device: int):
 
 
 def _device_of(t, name: str) -> int:
-    if not t.is_cuda:
+    try:
+        cuda = t.is_cuda
+    except AttributeError:
+        raise _no_tensor(t, name) from None
+    if not cuda:
         raise ValueError(f"{name} must be a device tensor (got {t.device})")
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions (got {tuple(t.shape)})")

@@ -166,3 +166,18 @@ def test_binding_refuses_host_tensors():
         S.act_alloc(4, 64, "cpu")
     with pytest.raises(S.ScapeError):
         S.act_alloc(4, 0, "cpu")
+
+
+def test_binding_refuses_what_is_not_a_tensor():
+    """A missing or foreign argument is named, before anything is called."""
+    x, vec = torch.zeros(4, 64), torch.zeros(64)
+    for bad, name in ((lambda: S.act_pack(None, None), "x"), (lambda: S.act_unpack(None, x), "a"),
+                      (lambda: S.rmsnorm_pack(None, vec, 1e-5, y=x), "x"),
+                      (lambda: S.rmsnorm_backward(None, None, vec, vec, x, vec, vec), "dy"),
+                      (lambda: S.wgrad(None, None, x, vec), "dy"), (lambda: S.wgrad([1.0], None, x, vec), "dy"),
+                      (lambda: S.wgrad_workspace_bytes(4, 64, 64, 3.0), "dy"),
+                      (lambda: S._workspace(None, 256, 0), "workspace"), (lambda: S._matrix(2.0, "y", 4, 64, 0), "y"),
+                      (lambda: S._vector([0.0] * 64, "weight", 64, 0), "weight"),
+                      (lambda: S.ActCheckpoint(None, None, 64), "codes")):
+        with pytest.raises(ValueError, match=name):
+            bad()
