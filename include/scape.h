@@ -511,8 +511,8 @@ scape_status scape_rmsnorm_backward(int64_t rows, int64_t cols, scape_matrix dy,
                                     hipStream_t stream);
 
 /* Bytes of scratch scape_wgrad needs with this dy (256-byte aligned): the
- * checkpoint in 16 bits, dy's terms (none for a 16-bit dy of 16-byte aligned
- * rows with out % 8 == 0) and partial sums.  dy.data null: enough for any dy.
+ * checkpoint in 16 bits (for fp16 with its columns' scales), dy's terms (none
+ * for a 16-bit dy of 16-byte aligned rows with out % 8 == 0) and partial sums.  dy.data null: enough for any dy.
  * 0 if a size is invalid. */
 size_t scape_wgrad_workspace_bytes(int64_t rows, int64_t in, int64_t out, scape_matrix dy);
 

@@ -89,3 +89,33 @@ def test_wgrad_fp16_rows_of_unlike_size(S):
     S.wgrad(dy.t, fill_act(S, q, s, n_in), dw, ws)
     want, _ = A.wgrad(dyn, A.unpack(q, s, n_in))
     assert (want.astype(np.float32) == want).all() and (f32(dw) == want).all()
+
+
+@pytest.mark.parametrize("rows,n_in,n_out", [(700, 200, 136), (3000, 136, 200)])
+def test_wgrad_fp16_captured_with_other_scales(S, rows, n_in, n_out):
+    """A captured call finds the scales of what lies in its buffers when it is
+    replayed, in a workspace that other calls have used in between."""
+    dt = torch.float16
+    first = exact_inputs(rows, n_in, n_out, "fp16", 1)
+    a, dy = fill_act(S, first[0], first[1], n_in), torch.from_numpy(first[2]).to(DEV, dt)
+    ws = torch.empty(S.wgrad_workspace_bytes(rows, n_in, n_out, dy), dtype=torch.uint8, device=DEV)
+    dw, db = torch.empty(n_out, n_in, device=DEV), torch.empty(n_out, device=DEV)
+    S.wgrad(dy, a, dw, ws, dbias=db)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        S.wgrad(dy, a, dw, ws, dbias=db)
+    for i, shift in enumerate((0, -90, 70, -40)):
+        q, s, dyn = exact_inputs(rows, n_in, n_out, "fp16", 10 + i)
+        s = np.where(s == 0, 0, s.astype(np.int64) + shift + 20 * (np.arange(s.shape[1]) % 3)).astype(np.uint8)
+        a.codes.copy_(torch.from_numpy(q))
+        a.scales.copy_(torch.from_numpy(s))
+        dy.copy_(torch.from_numpy(dyn))
+        dw.fill_(-1.0)
+        db.fill_(-1.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        want, wb = A.wgrad(dyn, A.unpack(q, s, n_in))
+        assert (want.astype(np.float32) == want).all()
+        assert (f32(dw) == want).all() and (f32(db) == wb).all(), i
+        ws.fill_(0xFF)
