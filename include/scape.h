@@ -541,6 +541,135 @@ scape_status scape_wgrad(int64_t rows, int64_t in, int64_t out, scape_matrix dy,
                          float* dw, float* dbias, int32_t accumulate, void* workspace, size_t workspace_bytes,
                          hipStream_t stream);
 
+/*
+ * ---- The ends of a training step: embedding, log probabilities, clipping ----
+ * The operators before the first layer, behind the last one, and between the
+ * backward pass and the step.  Matrices, limits and the rules on overlapping
+ * and on gradient rows are those of the activation operators; sizes called
+ * vocab or positions count rows of a table or columns of logits.  Results are
+ * deterministic: no sum depends on the order in which workgroups run.
+ */
+
+/* Token numbers: a contiguous device array of 32- or 64-bit signed integers,
+ * aligned to their size.  A number outside [0, vocab) is no token (padding). */
+typedef struct {
+  const void* data;
+  int32_t bits; /* 32 or 64 */
+} scape_ids;
+
+/*
+ * Rows of an embedding table by token:
+ *   out[t] = scale * table[ids[t]] + pos_table[pos[t]]
+ * in fp32, rounded to out's type; no token, or no position: zero in that
+ * row's place.  table is [vocab][cols], pos_table [positions][cols] of table's
+ * type (data null: no second table, pos and positions are not looked at), out
+ * [tokens][cols].
+ * 1 <= vocab, positions < 2^31, 0 <= tokens < 2^31.
+ */
+scape_status scape_embed(int64_t tokens, int64_t vocab, int64_t positions, int64_t cols, scape_ids ids,
+                         scape_matrix table, float scale, scape_ids pos, scape_matrix pos_table, scape_matrix out,
+                         hipStream_t stream);
+
+/* Bytes of scratch scape_embed_backward needs (256-byte aligned).  0 if a
+ * size is invalid. */
+size_t scape_embed_workspace_bytes(int64_t tokens, int64_t cols);
+
+/*
+ * Gradient of such a table from that of the rows:
+ *   dtable[v] = scale * sum over t with ids[t] = v of dy[t]
+ * added to what dtable holds if accumulate is not 0 (rows of no token then
+ * stay as they are; otherwise they are set to zero).  dtable is contiguous
+ * fp32 [vocab][cols], and may be a tensor's part of a row of grads.  dy of no
+ * token is not read.  Sums are fp32, of at most a few dozen rows each, joined
+ * in the tokens' order.  A table of positions takes a call of its own, with
+ * pos in the place of ids.
+ */
+scape_status scape_embed_backward(int64_t tokens, int64_t vocab, int64_t cols, scape_ids ids, scape_matrix dy,
+                                  float scale, float* dtable, int32_t accumulate, void* workspace,
+                                  size_t workspace_bytes, hipStream_t stream);
+
+/* Most alternatives a row of logits can be asked for (64). */
+int32_t scape_token_logprobs_max_top(void);
+
+/* Bytes of scratch scape_token_logprobs needs (256-byte aligned).  0 if a
+ * size is invalid. */
+size_t scape_token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int32_t top);
+
+/*
+ * Log probabilities of given tokens under the softmax of z = scale * logits
+ * (1 / scale: the temperature), logits [rows][vocab].  Per row, with m the
+ * largest logit, o the sum over all words but one of the likeliest of
+ * e^(scale (x - m)), and log-sum s = log(1 + o):
+ *   logp     [rows]       scale (x_y - m) - s, y = targets[row]; 0 for no token
+ *   stats    [rows][2]    m, s
+ *   entropy  [rows]       -sum p log p
+ *   top_ids  i32[rows][top], top_logp [rows][top]: the `top` likeliest words and
+ *            their log probabilities, by logit from the largest down, equal
+ *            logits by index from the lowest up (NaN before everything else)
+ *   dlogits  [rows][vocab], logits' type: the gradient of
+ *            sum over rows of dlogp[r] * logp[r] + dentropy[r] * entropy[r],
+ *              scale * (dlogp (1[j = y] - p_j) - dentropy p_j (log p_j + entropy)).
+ *            dlogp is taken as 0 where the target is no token; a row whose
+ *            dlogp and dentropy are both 0 gets zeros, whatever its logits are.
+ * Each output is left out if null, but one has to be there; targets may be
+ * null if neither logp nor dlogp is asked for; top 0 goes with null lists.
+ * With dlogits at least one of dlogp and dentropy is needed (null: zeros);
+ * without it both have to be null.  dlogits may be logits' own matrix (same
+ * data and ld).  1 <= vocab <= 2^20, 0 <= top <= min(vocab, 64), scale positive
+ * and finite.
+ *
+ * Sums are fp32.  o is summed apart from the 1 it is added to, so logp and
+ * entropy keep their relative precision where one word is all but certain.  A
+ * row whose logits are all -inf has logp and top_logp -inf, entropy 0 and a zero
+ * gradient; one that holds a NaN or +inf has NaN for all of them.
+ */
+scape_status scape_token_logprobs(int64_t rows, int64_t vocab, scape_matrix logits, float scale, scape_ids targets,
+                                  float* logp, float* stats, float* entropy, int32_t top, float* top_logp,
+                                  int32_t* top_ids, const float* dlogp, const float* dentropy, scape_matrix dlogits,
+                                  void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The same dlogits in a call of its own, where dlogp or dentropy depends on
+ * what the first call gave: from its stats and (with dentropy) entropy. */
+scape_status scape_token_logprobs_backward(int64_t rows, int64_t vocab, scape_matrix logits, float scale,
+                                           scape_ids targets, const float* stats, const float* entropy,
+                                           const float* dlogp, const float* dentropy, scape_matrix dlogits,
+                                           hipStream_t stream);
+
+/* One gradient tensor of a list: count elements of type dtype at data, and
+ * where its clipped values go: out of type out_dtype (dtype or fp32), which
+ * may be data itself (then out_dtype = dtype).  out null: data itself. */
+typedef struct {
+  const void* data;
+  void* out;
+  int64_t count;
+  int32_t dtype;
+  int32_t out_dtype;
+} scape_grad;
+
+/* Bytes of scratch of the two calls below for this list (256-byte aligned).
+ * 0 if it is invalid.  The list itself is HOST memory, read during the call. */
+size_t scape_grad_workspace_bytes(int32_t count, const scape_grad* grads, int32_t groups);
+
+/*
+ * Norm of gradients over many tensors: the list is cut into `groups` equal
+ * consecutive parts (count % groups == 0; one a worker, say), and
+ *   norm[g] = scale * sqrt(sum over the tensors of part g of their squares)
+ * scale (positive, finite) undoes a loss scale or a number of micro-batches.
+ * Squares and sums are binary64, so no square overflows or is lost.
+ */
+scape_status scape_grad_norm(int32_t count, const scape_grad* grads, int32_t groups, float scale, float* norm,
+                             void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Clipping by that norm:
+ *   out = data * (scale * min(1, max_norm / norm[g]))
+ * rounded once; norm [groups] is written as above.  A part whose norm is not
+ * finite is scaled and not clipped.  In place, a part with the factor 1 is not
+ * written.  max_norm is positive (infinite: scale only).
+ */
+scape_status scape_grad_clip(int32_t count, const scape_grad* grads, int32_t groups, float scale, float max_norm,
+                             float* norm, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* -------------------------------------------------------------- utility */
 
 const char* scape_status_string(scape_status s);

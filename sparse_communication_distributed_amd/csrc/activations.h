@@ -207,6 +207,14 @@ __device__ __forceinline__ void store8(void* p, int64_t row0, int64_t c, int64_t
   }
 }
 
+// Sum over a wave; every lane gets it, the same one.
+template <typename V>
+__device__ __forceinline__ V wave_sum(V x) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d, 64);
+  return x;
+}
+
 // Maximum over the 4 lanes of a quad (one block of 32 columns, 8 a lane).
 __device__ __forceinline__ uint32_t quad_max(uint32_t x) {
   uint32_t y = (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xB1, 0xf, 0xf, true);  // lanes 1 0 3 2

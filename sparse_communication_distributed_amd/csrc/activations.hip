@@ -89,12 +89,6 @@ unsigned walk_grid(int64_t rows, int64_t nblk) {
 
 // Sum over the T threads (64: a wave; more: the workgroup) that share a row;
 // every thread gets it, the same one.
-template <typename V>
-__device__ __forceinline__ V wave_sum(V x) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d, 64);
-  return x;
-}
 template <int T, typename V>
 __device__ __forceinline__ V row_sum(V x, V* lds) {
   x = wave_sum(x);

@@ -50,6 +50,16 @@ class ActView(ctypes.Structure):
     _fields_ = [("codes", c_void_p), ("scales", c_void_p)]
 
 
+class Ids(ctypes.Structure):
+    """scape_ids: token numbers, 32- or 64-bit."""
+    _fields_ = [("data", c_void_p), ("bits", c_int32)]
+
+
+class Grad(ctypes.Structure):
+    """scape_grad: one tensor of a list of gradients, and its clipped place."""
+    _fields_ = [("data", c_void_p), ("out", c_void_p), ("count", c_int64), ("dtype", c_int32), ("out_dtype", c_int32)]
+
+
 class ScapeError(RuntimeError):
     def __init__(self, status: int, detail: str):
         self.status = status
@@ -109,6 +119,21 @@ _SIGS = {
                                      ctypes.POINTER(c_int32)]),
     "scape_wgrad": (c_int, [c_int64, c_int64, c_int64, Matrix, ActView, c_void_p, c_void_p, c_void_p, c_int32,
                             c_void_p, c_size_t, c_void_p]),
+    "scape_embed": (c_int, [c_int64, c_int64, c_int64, c_int64, Ids, Matrix, c_float, Ids, Matrix, Matrix, c_void_p]),
+    "scape_embed_workspace_bytes": (c_size_t, [c_int64, c_int64]),
+    "scape_embed_backward": (c_int, [c_int64, c_int64, c_int64, Ids, Matrix, c_float, c_void_p, c_int32, c_void_p,
+                                     c_size_t, c_void_p]),
+    "scape_token_logprobs_max_top": (c_int32, []),
+    "scape_token_logprobs_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int32]),
+    "scape_token_logprobs": (c_int, [c_int64, c_int64, Matrix, c_float, Ids, c_void_p, c_void_p, c_void_p, c_int32,
+                                     c_void_p, c_void_p, c_void_p, c_void_p, Matrix, c_void_p, c_size_t, c_void_p]),
+    "scape_token_logprobs_backward": (c_int, [c_int64, c_int64, Matrix, c_float, Ids, c_void_p, c_void_p, c_void_p,
+                                              c_void_p, Matrix, c_void_p]),
+    "scape_grad_workspace_bytes": (c_size_t, [c_int32, ctypes.POINTER(Grad), c_int32]),
+    "scape_grad_norm": (c_int, [c_int32, ctypes.POINTER(Grad), c_int32, c_float, c_void_p, c_void_p, c_size_t,
+                                c_void_p]),
+    "scape_grad_clip": (c_int, [c_int32, ctypes.POINTER(Grad), c_int32, c_float, c_float, c_void_p, c_void_p, c_size_t,
+                                c_void_p]),
     "scape_status_string": (c_char_p, [c_int]),
     "scape_last_error": (c_char_p, []),
     "scape_profile_stages": (c_int, []),
@@ -715,6 +740,221 @@ def wgrad(dy, x: ActCheckpoint, dw, workspace, gain=None, dbias=None, accumulate
              _vector(dbias, "dbias", n_out, dev), 1 if accumulate else 0, ws, have)
 
 
+# ------------------------- ends of a step: tokens, probabilities, clipping
+
+_NO_IDS = Ids(None, 0)
+_ID_BITS = None
+
+
+def _ids(t, name: str, count: int, device: int) -> Ids:
+    """Token numbers: a contiguous int32 or int64 device tensor of `count`
+    elements; None: none."""
+    global _ID_BITS
+    if t is None:
+        return _NO_IDS
+    try:
+        at = t.get_device()
+    except AttributeError:
+        raise _no_tensor(t, name) from None
+    if _ID_BITS is None:
+        import torch
+        _ID_BITS = {torch.int32: 32, torch.int64: 64}
+    bits = _ID_BITS.get(t.dtype)
+    if bits is None:
+        raise ValueError(f"{name} must be int32 or int64 (got {t.dtype})")
+    if at != device:
+        raise ValueError(f"{name} must be a tensor on device {device} (got {t.device})")
+    if not t.is_contiguous() or t.numel() != count:
+        raise ValueError(f"{name} must be contiguous with {count} elements (got {tuple(t.shape)})")
+    return Ids(t.data_ptr(), bits)
+
+
+def _int_list(t, name: str, rows: int, cols: int, device: int) -> Optional[int]:
+    """Address of a contiguous int32 device tensor [rows][cols]."""
+    if t is None:
+        return None
+    try:
+        at = t.get_device()
+    except AttributeError:
+        raise _no_tensor(t, name) from None
+    import torch
+    if at != device or t.dtype != torch.int32:
+        raise ValueError(f"{name} must be an int32 tensor on device {device} (got {t.dtype} on {t.device})")
+    if not t.is_contiguous() or t.shape != (rows, cols):
+        raise ValueError(f"{name} must be contiguous of shape ({rows}, {cols}) (got {tuple(t.shape)})")
+    return t.data_ptr()
+
+
+def embed(ids, table, out, scale: float = 1.0, pos=None, pos_table=None, stream=None) -> None:
+    """out[t] = scale * table[ids[t]] + pos_table[pos[t]], rounded to out's
+    type: rows of table [vocab][cols] by token (int32 or int64, any shape of
+    as many elements as out has rows), and of pos_table [positions][cols] by
+    position if there is one.  A number outside its table stands for zero."""
+    dev = _device_of(table, "table")
+    vocab, cols = table.shape
+    _device_of(out, "out")
+    tokens = out.shape[0]
+    positions = 0
+    if pos_table is not None:
+        _device_of(pos_table, "pos_table")
+        positions = pos_table.shape[0]
+    elif pos is not None:
+        raise ValueError("pos needs pos_table")
+    _enqueue(dev, stream, lib().scape_embed, tokens, vocab, positions, cols, _ids(ids, "ids", tokens, dev),
+             _matrix(table, "table", vocab, cols, dev), scale, _ids(pos, "pos", tokens, dev),
+             _matrix(pos_table, "pos_table", positions, cols, dev), _matrix(out, "out", tokens, cols, dev))
+
+
+def embed_workspace_bytes(tokens: int, cols: int) -> int:
+    return int(lib().scape_embed_workspace_bytes(tokens, cols))
+
+
+def embed_backward(ids, dy, dtable, workspace, scale: float = 1.0, accumulate: bool = False, stream=None) -> None:
+    """Gradient of an embedding table, dtable [vocab][cols] (fp32, may be a
+    part of a row of the optimizer's gradients), from that of its rows, dy
+    [tokens][cols]: every row of dtable set, or (with accumulate) the rows of
+    the tokens added to."""
+    dev = _device_of(dy, "dy")
+    tokens, cols = dy.shape
+    _device_of(dtable, "dtable")
+    vocab = dtable.shape[0]
+    if dtable.shape[1] != cols:
+        raise ValueError(f"dtable must have {cols} columns (got {tuple(dtable.shape)})")
+    ws, have = _workspace(workspace, embed_workspace_bytes(tokens, cols), dev)
+    _enqueue(dev, stream, lib().scape_embed_backward, tokens, vocab, cols, _ids(ids, "ids", tokens, dev),
+             _matrix(dy, "dy", tokens, cols, dev), scale, _vector(dtable, "dtable", vocab * cols, dev),
+             1 if accumulate else 0, ws, have)
+
+
+def token_logprobs_max_top() -> int:
+    return int(lib().scape_token_logprobs_max_top())
+
+
+def token_logprobs_workspace_bytes(rows: int, vocab: int, top: int = 0) -> int:
+    return int(lib().scape_token_logprobs_workspace_bytes(rows, vocab, top))
+
+
+def token_logprobs(logits, targets, logp, workspace, stats=None, entropy=None, top_logp=None, top_ids=None,
+                   scale: float = 1.0, dlogp=None, dentropy=None, dlogits=None, stream=None) -> None:
+    """Log probabilities logp [rows] of `targets` under softmax(scale *
+    logits [rows][vocab]), with what else is asked for: the rows' stats
+    [rows][2] and entropy [rows], their likeliest words top_ids (int32) and
+    top_logp [rows][top], and, where the weights of the log probabilities
+    (dlogp [rows]) and entropies (dentropy [rows]) are known before, the
+    gradient dlogits (which may be logits itself).  A target outside the
+    vocabulary has logp 0 and no gradient."""
+    dev = _device_of(logits, "logits")
+    rows, vocab = logits.shape
+    lists = top_ids if top_ids is not None else top_logp
+    top = 0
+    if lists is not None:
+        _device_of(lists, "top_ids" if top_ids is not None else "top_logp")
+        top = lists.shape[1]
+        if top_logp is not None and top_logp.shape != (rows, top):
+            raise ValueError(f"top_logp must have shape ({rows}, {top}) (got {tuple(top_logp.shape)})")
+    ws, have = _workspace(workspace, token_logprobs_workspace_bytes(rows, vocab, top), dev)
+    _enqueue(dev, stream, lib().scape_token_logprobs, rows, vocab, _matrix(logits, "logits", rows, vocab, dev), scale,
+             _ids(targets, "targets", rows, dev), _vector(logp, "logp", rows, dev),
+             _vector(stats, "stats", 2 * rows, dev), _vector(entropy, "entropy", rows, dev), top,
+             _vector(top_logp, "top_logp", rows * top, dev), _int_list(top_ids, "top_ids", rows, top, dev),
+             _vector(dlogp, "dlogp", rows, dev), _vector(dentropy, "dentropy", rows, dev),
+             _matrix(dlogits, "dlogits", rows, vocab, dev), ws, have)
+
+
+def token_logprobs_backward(logits, targets, stats, dlogits, dlogp=None, entropy=None, dentropy=None,
+                            scale: float = 1.0, stream=None) -> None:
+    """The gradient dlogits of token_logprobs in a call of its own, from the
+    stats (and entropy) that it gave."""
+    dev = _device_of(logits, "logits")
+    rows, vocab = logits.shape
+    _enqueue(dev, stream, lib().scape_token_logprobs_backward, rows, vocab,
+             _matrix(logits, "logits", rows, vocab, dev), scale, _ids(targets, "targets", rows, dev),
+             _vector(stats, "stats", 2 * rows, dev), _vector(entropy, "entropy", rows, dev),
+             _vector(dlogp, "dlogp", rows, dev), _vector(dentropy, "dentropy", rows, dev),
+             _matrix(dlogits, "dlogits", rows, vocab, dev))
+
+
+class GradList:
+    """A list of gradient tensors (contiguous fp32, bf16 or fp16 tensors of
+    one device, any shapes), cut into `groups` equal consecutive parts that
+    have a norm each, one a worker, say.  ``out``: where clip_grads puts the
+    clipped values, tensors of as many elements and of the gradients' type or
+    fp32, for instance parts of the optimizer's gradient rows; None: in place.
+    It holds the tensors, not their values: a program that gets new gradient
+    tensors makes a new list."""
+
+    __slots__ = ("grads", "out", "groups", "device", "items")
+
+    def __init__(self, grads, out=None, groups: int = 1):
+        self.grads, self.groups = list(grads), int(groups)
+        self.out = None if out is None else list(out)
+        if not self.grads:
+            raise ValueError("grads is empty")
+        if self.groups < 1 or len(self.grads) % self.groups:
+            raise ValueError(f"{len(self.grads)} tensors cannot be cut into {self.groups} equal parts")
+        if self.out is not None and len(self.out) != len(self.grads):
+            raise ValueError(f"out must have {len(self.grads)} tensors (got {len(self.out)})")
+        self.items = (Grad * len(self.grads))()
+        self.device = None
+        for i, g in enumerate(self.grads):
+            dt = self._check(g, f"grads[{i}]")
+            item = self.items[i]
+            item.data, item.count, item.dtype = g.data_ptr() or None, g.numel(), dt
+            if self.out is None:
+                continue
+            o = self.out[i]
+            item.out_dtype = self._check(o, f"out[{i}]")
+            item.out = o.data_ptr() or None
+            if o.numel() != g.numel():
+                raise ValueError(f"out[{i}] must have {g.numel()} elements (got {o.numel()})")
+            if item.out_dtype not in (dt, 0):
+                raise ValueError(f"out[{i}] must be {g.dtype} or float32 (got {o.dtype})")
+
+    def _check(self, t, name: str) -> int:
+        try:
+            at = t.get_device()
+        except AttributeError:
+            raise _no_tensor(t, name) from None
+        if at < 0:
+            raise ValueError(f"{name} must be a device tensor (got {t.device})")
+        if self.device is None:
+            self.device = at
+        if at != self.device:
+            raise ValueError(f"{name} must be a tensor on device {self.device} (got {t.device})")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return _dtype(t.dtype, name)
+
+
+def _grad_list(grads) -> GradList:
+    if not isinstance(grads, GradList):
+        raise ValueError(f"grads must be a GradList (got {type(grads).__name__})")
+    return grads
+
+
+def grad_workspace_bytes(grads: GradList) -> int:
+    g = _grad_list(grads)
+    return int(lib().scape_grad_workspace_bytes(len(g.grads), g.items, g.groups))
+
+
+def grad_norm(grads: GradList, norm, workspace, scale: float = 1.0, stream=None) -> None:
+    """norm [groups] = scale * the 2-norm of each part of the list."""
+    g = _grad_list(grads)
+    ws, have = _workspace(workspace, grad_workspace_bytes(g), g.device)
+    _enqueue(g.device, stream, lib().scape_grad_norm, len(g.grads), g.items, g.groups, scale,
+             _vector(norm, "norm", g.groups, g.device), ws, have)
+
+
+def clip_grads(grads: GradList, max_norm: float, norm, workspace, scale: float = 1.0, stream=None) -> None:
+    """Writes every gradient times scale * min(1, max_norm / its part's norm)
+    to its place in out (or its own), and the norms to norm [groups].  A part
+    whose norm is not finite is scaled and not clipped."""
+    g = _grad_list(grads)
+    ws, have = _workspace(workspace, grad_workspace_bytes(g), g.device)
+    _enqueue(g.device, stream, lib().scape_grad_clip, len(g.grads), g.items, g.groups, scale, max_norm,
+             _vector(norm, "norm", g.groups, g.device), ws, have)
+
+
 # ---------------------------------------------------------------- profiling
 
 
@@ -784,7 +1024,10 @@ class ScapeOptimizer:
     rebuilt every step); with ``store_v`` the step also writes the
     uncorrected v_t at the masked entries into ``v`` [n], else ``v`` is
     None.  With ``count_nonfinite`` each step first counts the non-finite
-    values of its gradients on the device (``nonfinite_count()``)."""
+    values of its gradients on the device (``nonfinite_count()``).  With
+    ``max_norm`` a step clips each worker's row of its gradients in place by
+    that row's own norm before it uses them, and leaves the norms before the
+    clipping in ``grad_norm`` [K]."""
 
     def __init__(self, params, P: int, K: int, k: int, beta1=0.9, beta2=0.95, eps=1e-8,
                  weight_decay=0.0, lr=1e-3, device=None, store_v: bool = True, count_nonfinite: bool = False):
@@ -807,12 +1050,19 @@ class ScapeOptimizer:
         self.ws = torch.empty(wb, dtype=torch.uint8, device=dev)
         # debug switch: non-finite gradient values seen by the steps so far
         self.nonfinite = torch.zeros(1, dtype=torch.int64, device=dev) if count_nonfinite else None
+        self.grad_norm = torch.zeros(K, dtype=torch.float32, device=dev)
+        rows = (Grad * K)(*[Grad(self.e.data_ptr(), None, self.n, 0, 0)] * K)  # K fp32 rows of n, wherever they lie
+        self.clip_ws = torch.empty(int(lib().scape_grad_workspace_bytes(K, rows, K)), dtype=torch.uint8, device=dev)
         self.t = 0
 
-    def step(self, grads, stream=None) -> None:
+    def step(self, grads, stream=None, max_norm: Optional[float] = None) -> None:
         t = self.t + 1
         if self.nonfinite is not None:
             count_nonfinite(grads, self.nonfinite, self.K * self.n, stream)
+        if max_norm is not None:
+            _need(grads, "grads", self.K * self.n)
+            rows = grads.view(-1)[:self.K * self.n].view(self.K, self.n)
+            clip_grads(GradList(list(rows), groups=self.K), max_norm, self.grad_norm, self.clip_ws, stream=stream)
         step(self.d, self.params, grads, self.m, self.v, self.e, self.mask, self.k, self.bt, self.lr,
              t, self.ws, stream)
         self.t = t  # a rejected call leaves the step count unchanged
