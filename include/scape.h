@@ -564,7 +564,7 @@ typedef struct {
  * row's place.  table is [vocab][cols], pos_table [positions][cols] of table's
  * type (data null: no second table, pos and positions are not looked at), out
  * [tokens][cols].
- * 1 <= vocab, positions < 2^31, 0 <= tokens < 2^31.
+ * 1 <= vocab, positions < 2^31, 0 <= tokens <= 2^26.
  */
 scape_status scape_embed(int64_t tokens, int64_t vocab, int64_t positions, int64_t cols, scape_ids ids,
                          scape_matrix table, float scale, scape_ids pos, scape_matrix pos_table, scape_matrix out,
@@ -580,8 +580,8 @@ size_t scape_embed_workspace_bytes(int64_t tokens, int64_t cols);
  * added to what dtable holds if accumulate is not 0 (rows of no token then
  * stay as they are; otherwise they are set to zero).  dtable is contiguous
  * fp32 [vocab][cols], and may be a tensor's part of a row of grads.  dy of no
- * token is not read.  Sums are fp32, of at most a few dozen rows each, joined
- * in the tokens' order.  A table of positions takes a call of its own, with
+ * token is not read.  Sums are fp32, of at most a few dozen rows each, which are
+ * joined in the tokens' order.  A table of positions takes a call of its own, with
  * pos in the place of ids.
  */
 scape_status scape_embed_backward(int64_t tokens, int64_t vocab, int64_t cols, scape_ids ids, scape_matrix dy,

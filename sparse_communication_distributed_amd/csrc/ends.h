@@ -5,6 +5,8 @@
 
 namespace scape {
 
+constexpr int64_t kMaxTokens = int64_t(1) << 26;
+
 hipError_t launch_embed(int64_t tokens, int64_t vocab, int64_t positions, int64_t cols, const scape_ids& ids,
                         const scape_matrix& table, float scale, const scape_ids& pos, const scape_matrix& pos_table,
                         const scape_matrix& out, hipStream_t s);

@@ -19,9 +19,9 @@ scape_status check_ids(const char* name, const scape_ids& ids, int64_t count, bo
 }
 
 scape_status check_embed_size(int64_t tokens, int64_t vocab, int64_t cols) {
-  if (!rows_ok(tokens) || !table_ok(vocab) || !cols_ok(cols))
+  if (tokens < 0 || tokens > kMaxTokens || !table_ok(vocab) || !cols_ok(cols))
     return fail(SCAPE_ESHAPE,
-                "invalid shape: tokens=%lld vocab=%lld cols=%lld (need 0<=tokens<2^31, 1<=vocab<2^31, 1<=cols<=2^20)",
+                "invalid shape: tokens=%lld vocab=%lld cols=%lld (need 0<=tokens<=2^26, 1<=vocab<2^31, 1<=cols<=2^20)",
                 (long long)tokens, (long long)vocab, (long long)cols);
   return SCAPE_OK;
 }
@@ -118,7 +118,7 @@ scape_status scape_embed(int64_t tokens, int64_t vocab, int64_t positions, int64
 }
 
 size_t scape_embed_workspace_bytes(int64_t tokens, int64_t cols) {
-  if (!rows_ok(tokens) || !cols_ok(cols)) return 0;
+  if (tokens < 0 || tokens > kMaxTokens || !cols_ok(cols)) return 0;
   return embed_workspace(tokens, cols);
 }
 

@@ -40,7 +40,7 @@ EMBED = dict(tokens=4, vocab=9, positions=0, cols=64, ids=ids(), table=mat(), sc
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(tokens=-1), SHAPE), (dict(tokens=1 << 31), SHAPE), (dict(vocab=0), SHAPE), (dict(vocab=1 << 31), SHAPE),
+    (dict(tokens=-1), SHAPE), (dict(tokens=(1 << 26) + 1), SHAPE), (dict(vocab=0), SHAPE), (dict(vocab=1 << 31), SHAPE),
     (dict(cols=0), SHAPE), (dict(cols=(1 << 20) + 1), SHAPE), (dict(ids=NO_IDS), INVALID),
     (dict(ids=ids(16)), INVALID), (dict(ids=ids(64, FAKE + 4)), INVALID), (dict(ids=ids(32, FAKE + 2)), INVALID),
     (dict(table=NONE), INVALID), (dict(table=mat(63)), SHAPE), (dict(table=mat(dtype=3)), INVALID),
@@ -156,7 +156,8 @@ def test_sizes():
     assert S.token_logprobs_max_top() == 64
     for rows, vocab, top in ((-1, 5, 0), (1 << 31, 5, 0), (1, 0, 0), (1, 5, 6), (1, 100, 65), (1, 5, -1)):
         assert S.token_logprobs_workspace_bytes(rows, vocab, top) == 0
-    assert S.embed_workspace_bytes(-1, 5) == 0 and S.embed_workspace_bytes(5, 0) == 0
+    for tokens, cols in ((-1, 5), ((1 << 26) + 1, 5), (5, 0)):
+        assert S.embed_workspace_bytes(tokens, cols) == 0
     for n in (0, 1, 16384):
         assert S.embed_workspace_bytes(n, 2048) % 256 == 0 and S.embed_workspace_bytes(n, 2048) > 0
         assert S.token_logprobs_workspace_bytes(n, 32000, 20) % 256 == 0
