@@ -49,81 +49,187 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(EmbedArgs a) {
 // its border to a partial row, and the partial rows of a word are joined in
 // order.  No atomics: the sums are the same every time.
 
-constexpr uint32_t kNoWord = 0xffffffffu;
-constexpr int kTileMax = 2048;  // tokens that a workgroup sorts in LDS
-constexpr int kSortThreads = 1024;
-constexpr unsigned kFillBlocks = 4096;
+constexpr uint32_t kNoWord = 0xfffffffeu;  // above every word, and 1 more is no overflow
+constexpr int kSortTile = 512;  // tokens that are sorted by counting
 constexpr int kBatch = 8;  // rows of dy on the way at a time
 
 struct SortArgs {
   int64_t tokens, vocab;
-  scape_ids ids;
-  int tile;         // a power of two
-  int32_t tiles;
-  uint32_t* word;   // [tiles * tile], each tile sorted
+  const void* ids;
+  int tile;       // a power of two, at least 64
+  int lanes;      // that count for one token
+  uint32_t* word;  // [tiles * tile], each tile sorted
   uint32_t* token;
-  float* fill;      // set to zero by the other workgroups
-  int64_t fill_n;
 };
 
-// Sorts (word, place) pairs of a tile by bitonic exchanges in LDS.  The pairs
-// that a wave exchanges at distances of 64 and less lie in a part of the tile
-// of its own, so only the larger distances need the workgroup's barrier.
-__device__ __forceinline__ void sort_tile(uint64_t* lds, int n) {
-  for (int k = 2; k <= n; k <<= 1) {
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      for (int i = threadIdx.x; i < n / 2; i += kSortThreads) {
-        const int lo = ((i & ~(j - 1)) << 1) | (i & (j - 1));
-        const uint64_t x = lds[lo], y = lds[lo + j];
-        if ((x > y) == ((lo & k) == 0)) {
-          lds[lo] = y;
-          lds[lo + j] = x;
-        }
-      }
-      if (j > 64) {
-        __syncthreads();
-      } else {
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-        if (j == 1 && k >= 128) __syncthreads();  // the next k exchanges across waves
-      }
+// Sorts tiles by counting: a token's place is the number of tokens of its tile
+// that come before it.  The comparisons do not wait for each other and spread
+// over the card: 6 us, where exchanges in one workgroup took 20 us for tiles of
+// 2048.  (Counting in larger tiles: 10 us at 2048, 22 us at 8192.)
+template <typename I>
+__global__ void __launch_bounds__(kThreads) embed_sort_kernel(SortArgs a) {
+  extern __shared__ uint32_t lds[];
+  const int per = kThreads / a.lanes;      // tokens of a workgroup
+  const int parts = a.tile / per;          // workgroups of a tile
+  const int64_t t0 = (int64_t)(blockIdx.x / parts) * a.tile;
+  // eight loads on the way at a time; past the end, the last token's word again
+  for (int i0 = threadIdx.x; i0 < a.tile; i0 += 8 * kThreads) {
+    int64_t id[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t t = t0 + i0 + j * kThreads;
+      id[j] = token_at<I>(a.ids, t < a.tokens ? t : a.tokens - 1);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + j * kThreads;
+      if (i < a.tile) lds[i] = t0 + i < a.tokens && id[j] >= 0 && id[j] < a.vocab ? (uint32_t)id[j] : kNoWord;
     }
   }
   __syncthreads();
+  const int p = (int)(blockIdx.x % parts) * per + threadIdx.x / a.lanes;
+  const uint32_t w = lds[p];
+  // tokens in front of p come before it if their word is at most w, those
+  // behind it if it is below w; four at a time, p's own four as if behind it
+  uint32_t place = 0;
+  const int l = threadIdx.x & (a.lanes - 1);
+#pragma unroll 4
+  for (int q = l; q < a.tile / 4; q += a.lanes) {
+    const u32x4 k = *reinterpret_cast<const u32x4*>(lds + 4 * q);
+    const uint32_t bound = w + (4 * q + 3 < p ? 1u : 0u);
+    place += (k[0] < bound) + (k[1] < bound) + (k[2] < bound) + (k[3] < bound);
+  }
+  for (int d = a.lanes >> 1; d >= 1; d >>= 1) place += __shfl_xor((int)place, d, 64);
+  for (int i = p & ~3; i < p; ++i) place += lds[i] == w;
+  if (l == 0) {
+    a.word[t0 + place] = w;
+    a.token[t0 + place] = (uint32_t)t0 + (uint32_t)p;
+  }
 }
 
-__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(SortArgs a) {
-  __shared__ uint64_t lds[kTileMax];
-  if ((int32_t)blockIdx.x < a.tiles) {
-    const int64_t t0 = (int64_t)blockIdx.x * a.tile;
-    for (int i = threadIdx.x; i < a.tile; i += kSortThreads) {
-      uint32_t w = kNoWord;
-      if (t0 + i < a.tokens) {
-        const int64_t id = token_at(a.ids, t0 + i);
-        if (id >= 0 && id < a.vocab) w = (uint32_t)id;
+// Sorts by slabs of the vocabulary, in one launch: a workgroup owns `slab`
+// words and goes through all tokens.  Its waves take a stretch of them each,
+// list those of the slab in LDS and count them by word; a token's place is the
+// number of tokens of lower words, of the same word in the stretches before,
+// and of the same word before it in its list.
+constexpr int kSlabThreads = 1024;
+constexpr int kSlabWaves = kSlabThreads / 64;
+constexpr int kSlabMax = 512;
+constexpr int64_t kSlabTokens = 16384;  // the lists' room
+constexpr int64_t kSlabs = 1024;        // workgroups at most: each goes through all tokens
+constexpr int kAhead = 8;               // tokens of a lane on the way at a time
+
+struct SlabArgs {
+  int64_t tokens, vocab, padded;
+  const void* ids;
+  int slab;        // words of a workgroup, at most kSlabMax
+  int stretch;     // tokens of a wave, a multiple of 64
+  uint32_t* word;  // [padded]
+  uint32_t* token;
+};
+
+// The word of a token number, or one above every word.
+__device__ __forceinline__ uint32_t word_of(int64_t id) { return (uint64_t)id >> 32 ? kNoWord : (uint32_t)id; }
+__device__ __forceinline__ uint32_t word_of(int32_t id) { return id < 0 ? kNoWord : (uint32_t)id; }
+
+__device__ __forceinline__ uint32_t lanes_below(uint64_t mask) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
+}
+
+template <typename I>
+__global__ void __launch_bounds__(kSlabThreads) embed_slab_kernel(SlabArgs a) {
+  extern __shared__ uint32_t lds[];  // [kSlabWaves][slab] counts, then places; [kSlabWaves][stretch] lists
+  __shared__ uint32_t first[kSlabThreads], wave_lower[kSlabWaves], wave_total[kSlabWaves];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const uint32_t lo = blockIdx.x * (uint32_t)a.slab;
+  const uint32_t words = (uint32_t)(a.vocab - lo < a.slab ? a.vocab - lo : a.slab);
+  uint32_t* const mine = lds + wave * a.slab;
+  uint32_t* const list = lds + kSlabWaves * a.slab + wave * a.stretch;
+  for (int i = lane; i < a.slab; i += 64) mine[i] = 0;
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+
+  const int from = wave * a.stretch;
+  const int left = (int)a.tokens - from;
+  const int own = left < a.stretch ? left : a.stretch;  // not positive: none
+  const I* const ids = static_cast<const I*>(a.ids) + from;
+  uint32_t lower = 0, listed = 0;
+  for (int t0 = lane; t0 - lane < own; t0 += 64 * kAhead) {
+    I id[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int t = t0 + j * 64;
+      id[j] = ids[t < own ? t : own - 1];
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int t = t0 + j * 64;
+      const uint32_t w = t < own ? word_of(id[j]) : kNoWord;
+      const uint32_t r = w - lo;
+      lower += w < lo ? 1 : 0;
+      const uint64_t in = __ballot(r < words);
+      if (in) {
+        if (r < words) {
+          list[listed + lanes_below(in)] = r << 16 | (uint32_t)t;
+          atomicAdd(&mine[r], 1u);  // of LDS; a sum of ones has no order
+        }
+        listed += (uint32_t)__popcll(in);
       }
-      lds[i] = (uint64_t)w << 32 | (uint32_t)i;
     }
-    __syncthreads();
-    sort_tile(lds, a.tile);
-    for (int i = threadIdx.x; i < a.tile; i += kSortThreads) {
-      a.word[t0 + i] = (uint32_t)(lds[i] >> 32);
-      a.token[t0 + i] = (uint32_t)t0 + (uint32_t)lds[i];
-    }
-    return;
   }
-  // 16-byte stores from the first aligned element on
-  const int64_t lead0 = (4 - (int64_t)(((uintptr_t)a.fill >> 2) & 3)) & 3;
-  const int64_t lead = lead0 < a.fill_n ? lead0 : a.fill_n;
-  const int64_t whole = (a.fill_n - lead) / 4;
-  const int64_t at = (int64_t)(blockIdx.x - a.tiles) * kSortThreads + threadIdx.x;
-  const int64_t step = (int64_t)(gridDim.x - a.tiles) * kSortThreads;
-  f32x4* body = reinterpret_cast<f32x4*>(a.fill + lead);
-  for (int64_t i = at; i < whole; i += step) body[i] = f32x4{0, 0, 0, 0};
-  if (at < lead) a.fill[at] = 0.0f;
-  const int64_t tail = lead + whole * 4 + at;
-  if (at < 4 && tail < a.fill_n) a.fill[tail] = 0.0f;
+  lower = wave_sum(lower);
+  if (lane == 0) wave_lower[wave] = lower;
+  __syncthreads();
+  // a word's tokens, the waves' shares of them, then the words before it
+  uint32_t sum = 0;
+  if (threadIdx.x < (unsigned)a.slab) {
+    for (int w = 0; w < kSlabWaves; ++w) {
+      const uint32_t n = lds[w * a.slab + threadIdx.x];
+      lds[w * a.slab + threadIdx.x] = sum;
+      sum += n;
+    }
+  }
+  uint32_t scan = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t y = __shfl_up(scan, d, 64);
+    if (lane >= d) scan += y;
+  }
+  if (lane == 63) wave_total[wave] = scan;
+  __syncthreads();
+  uint32_t base = 0, end = 0;
+  for (int w = 0; w < kSlabWaves; ++w) {
+    base += wave_lower[w] + (w < wave ? wave_total[w] : 0);
+    end += wave_lower[w] + wave_total[w];
+  }
+  first[threadIdx.x] = base + scan - sum;
+  __syncthreads();
+
+  for (uint32_t i0 = 0; i0 < listed; i0 += 64) {
+    const bool there = i0 + lane < listed;
+    const uint32_t e = there ? list[i0 + lane] : 0xffffffffu;
+    const uint32_t r = e >> 16;
+    for (uint64_t open = __ballot(there); open;) {
+      const uint32_t x = (uint32_t)__builtin_amdgcn_readlane((int)r, __builtin_ctzll(open));
+      const uint64_t same = __ballot(r == x);  // no slab has a word 0xffff
+      open &= ~same;
+      const uint32_t at = first[x] + mine[x] + lanes_below(same);
+      if (r == x) {
+        a.word[at] = lo + x;
+        a.token[at] = (uint32_t)from + (e & 0xffffu);
+      }
+      if (lane == 0) mine[x] += (uint32_t)__popcll(same);
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
+  }
+  if (blockIdx.x == gridDim.x - 1)  // the places behind the last word's
+    for (int64_t i = end + threadIdx.x; i < a.padded; i += kSlabThreads) {
+      a.word[i] = kNoWord;
+      a.token[i] = 0;
+    }
 }
 
 // Number of elements of a sorted run below w (or not above it).
@@ -182,7 +288,45 @@ struct ChunkArgs {
   bool accumulate;
   float* part;            // [chunks][2][pitch]: the first word's and the last word's sums
   int64_t pitch;
+  int64_t blocks;         // that sum chunks; the others clear rows of no token
+  int64_t vocab;
+  int rows;               // that a wave clears, below 64
+  bool stream;            // past the caches
 };
+
+// Clears those of a wave's rows that no token has: one look-up a lane finds
+// where each row's word would stand among the sorted ones, and neighbouring
+// rows without one are one range.
+__device__ __forceinline__ void clear_rows(const ChunkArgs& a, int64_t wave) {
+  const int lane = threadIdx.x & 63;
+  const int64_t v0 = wave * a.rows;
+  const int64_t rows = a.vocab - v0 < a.rows ? a.vocab - v0 : a.rows;
+  if (rows <= 0) return;
+  const int64_t n = (int64_t)a.chunks * a.chunk;
+  const int64_t at = lane <= rows ? below(a.word, n, (uint32_t)(v0 + lane), false) : 0;
+  const int64_t next = __shfl_down((long long)at, 1, 64);
+  uint64_t clear = __ballot(lane < rows && at == next);
+  while (clear) {
+    const int from = __builtin_ctzll(clear);
+    const uint64_t rest = ~(clear >> from);
+    const int count = rest ? __builtin_ctzll(rest) : 64;
+    clear &= count + from >= 64 ? 0 : ~0ull << (from + count);
+    float* const p = a.dtable + (v0 + from) * a.cols;
+    const int64_t size = count * a.cols;
+    // 16-byte stores from the first aligned element on
+    const int64_t lead0 = (4 - (int64_t)(((uintptr_t)p >> 2) & 3)) & 3;
+    const int64_t lead = lead0 < size ? lead0 : size;
+    const int64_t whole = (size - lead) / 4;
+    f32x4* body = reinterpret_cast<f32x4*>(p + lead);
+    if (a.stream) {
+      for (int64_t i = lane; i < whole; i += 64) __builtin_nontemporal_store(f32x4{0, 0, 0, 0}, body + i);
+    } else {
+      for (int64_t i = lane; i < whole; i += 64) body[i] = f32x4{0, 0, 0, 0};
+    }
+    if (lane < lead) p[lane] = 0.0f;
+    if (lane < 4 && lead + whole * 4 + lane < size) p[lead + whole * 4 + lane] = 0.0f;
+  }
+}
 
 __device__ __forceinline__ void put_row(const ChunkArgs& a, int64_t w, int64_t c, float (&v)[8]) {
   float* row = a.dtable;
@@ -201,6 +345,10 @@ __device__ __forceinline__ void put_row(const ChunkArgs& a, int64_t w, int64_t c
 
 template <int DT, bool WHOLE>
 __global__ void __launch_bounds__(kThreads) embed_chunk_kernel(ChunkArgs a) {
+  if ((int64_t)blockIdx.x >= a.blocks) {
+    clear_rows(a, ((blockIdx.x - a.blocks) * kThreads + threadIdx.x) >> 6);
+    return;
+  }
   const int64_t wave = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 6;
   const int lane = threadIdx.x & 63;
   const int64_t group = (wave / a.slabs) * (64 / a.lanes) + lane / a.lanes;
@@ -211,6 +359,7 @@ __global__ void __launch_bounds__(kThreads) embed_chunk_kernel(ChunkArgs a) {
   const uint32_t after = group + 1 < a.chunks ? a.word[p0 + a.chunk] : kNoWord;
   uint32_t cur = a.word[p0];
   if (cur == kNoWord) return;
+  const uint32_t first = a.token[p0];
   bool open = before == cur;  // cur's sum began in an earlier chunk
   float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   const auto flush = [&](bool last) {
@@ -223,25 +372,36 @@ __global__ void __launch_bounds__(kThreads) embed_chunk_kernel(ChunkArgs a) {
     }
     open = false;
   };
-  for (int b = 0; b < a.chunk; b += kBatch) {
-    uint32_t w[kBatch], t[kBatch];
-    __builtin_memcpy(w, a.word + p0 + b, 4 * kBatch);
-    __builtin_memcpy(t, a.token + p0 + b, 4 * kBatch);
-    if (w[0] == kNoWord) break;
+  // the rows of a batch are on the way while those of the one before are added
+  struct Batch {
+    uint32_t w[kBatch];
     Raw8<DT, WHOLE, false> r[kBatch];
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j)
-      r[j].load(a.dy, (int64_t)(w[j] == kNoWord ? t[0] : t[j]) * a.dy_ld, c, a.cols);
+  } now, next;
+  const auto fetch = [&](Batch& x, int b) {
+    uint32_t t[kBatch];
+    __builtin_memcpy(x.w, a.word + p0 + b, 4 * kBatch);
+    __builtin_memcpy(t, a.token + p0 + b, 4 * kBatch);
+    // no word: any token's row, which is left out of the sums
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      if (w[j] != cur) {
+      const uint32_t row = x.w[j] == kNoWord ? first : t[j];
+      x.r[j].load(a.dy, (int64_t)row * a.dy_ld, c, a.cols);
+    }
+  };
+  fetch(next, 0);
+  for (int b = 0; b < a.chunk; b += kBatch) {
+    now = next;
+    if (b + kBatch < a.chunk) fetch(next, b + kBatch);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (now.w[j] != cur) {
         if (cur != kNoWord) flush(false);
-        cur = w[j];
+        cur = now.w[j];
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
       }
       float v[8];
-      r[j].unpack(v);
+      now.r[j].unpack(v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[i] += v[i];
     }
@@ -254,16 +414,21 @@ __global__ void __launch_bounds__(kThreads) embed_chunk_kernel(ChunkArgs a) {
 // quarters.  A lane owns 4 columns.
 __device__ __forceinline__ void join_word(const ChunkArgs& a, int32_t k, f32x4 (*lds)[64]) {
   const int64_t p0 = (int64_t)k * a.chunk, p1 = p0 + a.chunk;
-  const uint32_t w = a.word[p1 - 1];
-  if (w == kNoWord || a.word[p1] != w) return;
-  if (a.word[p0] == w && p0 > 0 && a.word[p0 - 1] == w) return;  // begins further ahead
-  int64_t lo = p1, hi = (int64_t)a.chunks * a.chunk;  // the word's end
-  while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (a.word[mid] == w) lo = mid;
-    else hi = mid;
+  const uint32_t w = a.word[p1 - 1], after = a.word[p1], first = a.word[p0];
+  const uint32_t before = a.word[p0 > 0 ? p0 - 1 : 0];
+  const auto begin_of = [&](int64_t chunk) { return chunk < a.chunks ? a.word[chunk * a.chunk] : kNoWord; };
+  uint32_t begins = begin_of(k + 1 + (threadIdx.x & 63));
+  if (w == kNoWord || after != w) return;
+  if (first == w && p0 > 0 && before == w) return;  // begins further ahead
+  // partial rows: k's last, then the first of each chunk that begins with the word
+  int64_t n = 1;
+  for (int64_t at = k + 1;;) {
+    const uint64_t others = __ballot(begins != w);
+    n += others ? __builtin_ctzll(others) : 64;
+    if (others) break;
+    at += 64;
+    begins = begin_of(at + (threadIdx.x & 63));
   }
-  const int64_t n = lo / a.chunk - k + 1;  // partial rows: k's last, then the first of each chunk up to lo's
   const int q = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int64_t c = ((int64_t)blockIdx.y * 64 + lane) * 4;
   const bool mine = c < a.pitch;
@@ -294,7 +459,7 @@ __global__ void __launch_bounds__(kThreads) embed_join_kernel(ChunkArgs a) {
 
 // How a gradient's tokens are cut, and its workspace.
 struct BackPlan {
-  int tile, chunk, lanes;
+  int tile, count_lanes, chunk, lanes;
   int32_t tiles, chunks, slabs;
   int64_t padded, pitch;
   size_t word[2], token[2], part, bytes;  // offsets; the tiles go to the first pair, merges to and fro
@@ -303,7 +468,8 @@ struct BackPlan {
 BackPlan back_plan(int64_t tokens, int64_t cols) {
   BackPlan p;
   p.tile = 64;
-  while (p.tile < kTileMax && p.tile < tokens) p.tile *= 2;
+  while (p.tile < tokens && p.tile < kSortTile) p.tile *= 2;
+  p.count_lanes = 4;
   p.tiles = (int32_t)((tokens + p.tile - 1) / p.tile);
   p.padded = (int64_t)p.tiles * p.tile;
   const int64_t eights = (cols + 7) / 8;
@@ -346,6 +512,35 @@ void embed_out(const EmbedArgs& a, int out, hipStream_t s) {
   else embed_kernel<TT, SCAPE_F16><<<grid, kThreads, 0, s>>>(a);
 }
 
+// Words that a workgroup of the slab sort owns: about one workgroup a CU.  0:
+// sorted by tiles.  16384 tokens of 32000 words: slabs 7.5 us, tiles and their
+// merge 16.5; 1531 of 4099: 5.2 against 10.5.  The lists of more tokens do not
+// fit LDS, and more slabs than kSlabs would go through the tokens too often.
+int slab_of(int64_t tokens, int64_t vocab) {
+  int slab = 4;
+  while (slab < kSlabMax && (vocab + slab - 1) / slab > 256) slab *= 2;
+  return tokens <= kSlabTokens && (vocab + slab - 1) / slab <= kSlabs ? slab : 0;
+}
+
+// Sorts tiles and merges them; which pair of buffers holds the result.
+int sort_tiles(const BackPlan& p, int64_t tokens, int64_t vocab, const scape_ids& ids, char* base, hipStream_t s) {
+  const auto at = [&](size_t off) { return reinterpret_cast<uint32_t*>(base + off); };
+  const SortArgs sa{tokens, vocab, ids.data, p.tile, p.count_lanes, at(p.word[0]), at(p.token[0])};
+  const dim3 sorting((unsigned)(p.padded * p.count_lanes / kThreads));
+  if (ids.bits == 64) embed_sort_kernel<int64_t><<<sorting, kThreads, p.tile * 4, s>>>(sa);
+  else embed_sort_kernel<int32_t><<<sorting, kThreads, p.tile * 4, s>>>(sa);
+  int from = 0;
+  for (int64_t run = p.tile; run < p.padded; run *= kFan, from ^= 1) {
+    const int64_t runs = (p.padded + run - 1) / run;
+    int lanes = 1;
+    while (lanes < kFan && lanes < runs) lanes *= 2;
+    const dim3 grid(capped((p.padded * lanes + kThreads - 1) / kThreads, 1 << 22));
+    embed_merge_kernel<<<grid, kThreads, 0, s>>>(at(p.word[from]), at(p.token[from]), p.padded, run, lanes,
+                                                 at(p.word[from ^ 1]), at(p.token[from ^ 1]));
+  }
+  return from;
+}
+
 }  // namespace
 
 hipError_t launch_embed(int64_t tokens, int64_t vocab, int64_t positions, int64_t cols, const scape_ids& ids,
@@ -369,24 +564,28 @@ hipError_t launch_embed_backward(int64_t tokens, int64_t vocab, int64_t cols, co
   const BackPlan p = back_plan(tokens, cols);
   char* base = static_cast<char*>(ws);
   const auto at = [&](size_t off) { return reinterpret_cast<uint32_t*>(base + off); };
-  const SortArgs sa{tokens, vocab, ids, p.tile, p.tiles, at(p.word[0]), at(p.token[0]), dtable,
-                    accumulate ? 0 : vocab * cols};
-  const unsigned fill = capped((sa.fill_n / 4 + kSortThreads - 1) / kSortThreads + (sa.fill_n > 0), kFillBlocks);
-  embed_sort_kernel<<<dim3((unsigned)p.tiles + fill), kSortThreads, 0, s>>>(sa);
-  if (tokens == 0) return hipGetLastError();
   int from = 0;
-  for (int64_t run = p.tile; run < p.padded; run *= kFan, from ^= 1) {
-    const int64_t runs = (p.padded + run - 1) / run;
-    int lanes = 1;
-    while (lanes < kFan && lanes < runs) lanes *= 2;
-    const dim3 grid(capped((p.padded * lanes + kThreads - 1) / kThreads, 1 << 22));
-    embed_merge_kernel<<<grid, kThreads, 0, s>>>(at(p.word[from]), at(p.token[from]), p.padded, run, lanes,
-                                                 at(p.word[from ^ 1]), at(p.token[from ^ 1]));
+  const int slab = slab_of(tokens, vocab);
+  if (slab && tokens > 0) {
+    const int stretch = (int)((tokens + kSlabThreads - 1) / kSlabThreads) * 64;
+    const SlabArgs a{tokens, vocab, p.padded, ids.data, slab, stretch, at(p.word[0]), at(p.token[0])};
+    const dim3 grid((unsigned)((vocab + slab - 1) / slab));
+    const size_t lds = (size_t)(slab + stretch) * kSlabWaves * 4;
+    if (ids.bits == 64) embed_slab_kernel<int64_t><<<grid, kSlabThreads, lds, s>>>(a);
+    else embed_slab_kernel<int32_t><<<grid, kSlabThreads, lds, s>>>(a);
+  } else if (tokens > 0) {
+    from = sort_tiles(p, tokens, vocab, ids, base, s);
   }
-  const ChunkArgs ca{cols, at(p.word[from]), at(p.token[from]), p.chunk, p.chunks, p.lanes, p.slabs, dy.data, dy.ld,
-                     scale, dtable, accumulate, reinterpret_cast<float*>(base + p.part), p.pitch};
   const int64_t waves = ((int64_t)p.chunks * p.lanes + 63) / 64 * p.slabs;
-  const dim3 grid((unsigned)((waves + 3) / 4));
+  const int64_t blocks = (waves + 3) / 4;
+  // rows to clear: about 64 KB a wave
+  int64_t rows = (64 << 10) / (cols * 4);
+  rows = rows < 1 ? 1 : rows > 63 ? 63 : rows;
+  const int64_t clearing = accumulate ? 0 : (vocab + 4 * rows - 1) / (4 * rows);
+  const ChunkArgs ca{cols, at(p.word[from]), at(p.token[from]), p.chunk, p.chunks, p.lanes, p.slabs, dy.data, dy.ld,
+                     scale, dtable, accumulate, reinterpret_cast<float*>(base + p.part), p.pitch, blocks, vocab,
+                     (int)rows, vocab * cols * 4 > kStreamBytes};
+  const dim3 grid((unsigned)(blocks + clearing));
   if (dy.dtype == SCAPE_F32) launch_chunks<SCAPE_F32>(ca, grid, s);
   else if (dy.dtype == SCAPE_BF16) launch_chunks<SCAPE_BF16>(ca, grid, s);
   else launch_chunks<SCAPE_F16>(ca, grid, s);
