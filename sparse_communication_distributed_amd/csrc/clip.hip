@@ -2,129 +2,244 @@
 //
 // The tensors of a list go to the kernels by value, so that a call copies no
 // table to the device and can be captured.  Each is cut into pieces of one
-// size, a workgroup sums one piece, and the pieces' sums are added in their
+// size, a workgroup takes a piece, and the pieces' sums are added in their
 // order: no atomics, so results do not depend on the order of the workgroups.
+// Bound by memory: every gradient is read once for the norm and once for the
+// clipping, which begins with the pieces that were read last.
 #include "ends.h"
 
 namespace scape {
 namespace {
 
-constexpr int kSpans = 64;         // tensors of one launch
-constexpr int64_t kPieces = 4096;  // pieces of a long list, about
+constexpr int kSpans = 128;         // tensors of one launch: arguments of less than 4 KB
+constexpr int kLaunchGroups = 4096;  // groups of one launch: 12 bits
+constexpr int64_t kPieces = 16384;  // pieces of a long list, about
+constexpr int kFewPieces = 1024;   // of a group: the clipping adds their sums itself
 
 struct Span {
   const void* data;
   void* out;
-  int64_t count;
-  int32_t first;  // piece of the whole list at which it begins
-  int16_t dtype, out_dtype;
-  int32_t group;
+  uint64_t what;  // elements; from bit 48 on data's type, out's type, and the group less the launch's first
 };
 
 struct SpanArgs {
   Span span[kSpans];
-  int32_t n;
-  int32_t end;  // one past the last span's last piece
+  int32_t first[kSpans];  // piece of the whole list at which each span begins; past the last: none
+  int32_t begin;          // the first span's
+  int32_t end;            // one past the last span's last piece
+  int32_t group;          // of the first span
   int64_t piece;
   double* sums;
-  const double* factors;
+};
+
+struct Scaling {
+  const double* factors;  // of each group; null: found from the sums
+  float* norm;            // written where factors is null
+  float scale, max_norm;
+  int32_t group_pieces;  // where factors is null: of every group
+  bool stream;           // past the caches
 };
 
 struct GroupArgs {
   int32_t first[kSpans + 1];  // pieces of each group
-  int32_t n;
-  float scale, max_norm;
+  Scaling s;
   bool clip;
   const double* sums;
   double* factors;
   float* norm;
 };
 
+// Over the T threads of a workgroup; every one gets it, the same one.
+template <int T>
 __device__ __forceinline__ double block_sum(double x, double* lds) {
   x = wave_sum(x);
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
   __syncthreads();
   x = lds[0];
-  for (int w = 1; w < kThreads / 64; ++w) x += lds[w];
+#pragma unroll
+  for (int w = 1; w < T / 64; ++w) x += lds[w];
   return x;
 }
 
-// The span of a piece: the last one that begins at or before it and holds
-// anything (an empty tensor begins where the next one does).
+// Sum of a group's pieces.
+template <int T>
+__device__ __forceinline__ double group_sum(const double* sums, int32_t n, double* lds) {
+  double sum = 0.0;
+#pragma unroll 4
+  for (int32_t i = threadIdx.x; i < n; i += T) sum += sums[i];
+  return block_sum<T>(sum, lds);
+}
+
+__device__ __forceinline__ double factor_of(double norm, const Scaling& s) {
+  const bool over = norm > (double)s.max_norm && norm < (double)__builtin_inff();
+  return over ? (double)s.scale * ((double)s.max_norm / norm) : (double)s.scale;
+}
+
+// The span of a piece: the number of those that begin at or before it, less
+// one, counted by all lanes at once.
 __device__ __forceinline__ int span_of(const SpanArgs& a, int32_t piece) {
-  int lo = 0, hi = a.n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (a.span[mid].first <= piece) lo = mid;
-    else hi = mid;
+  const int lane = threadIdx.x & 63;
+  return __popcll(__ballot(a.first[lane] <= piece)) + __popcll(__ballot(a.first[64 + lane] <= piece)) - 1;
+}
+
+struct Piece {
+  const void* data;
+  void* out;
+  int64_t lo, hi;
+  int dtype, out_dtype, group;
+  __device__ __forceinline__ Piece(const SpanArgs& a, int32_t piece) {
+    const int span = span_of(a, piece);
+    const Span& s = a.span[span];
+    data = s.data;
+    out = s.out;
+    const int64_t count = (int64_t)(s.what & ((uint64_t(1) << 48) - 1));
+    dtype = (int)(s.what >> 48) & 3;
+    out_dtype = (int)(s.what >> 50) & 3;
+    group = a.group + (int)(s.what >> 52);
+    lo = (piece - a.first[span]) * a.piece;
+    hi = lo + a.piece < count ? lo + a.piece : count;
   }
-  return lo;
+};
+
+// N elements as they lie in memory: 8 or 16 bytes.
+template <int DT, int N>
+struct Some {
+  static constexpr int kBytes = N * (DT == SCAPE_F32 ? 4 : 2);
+  uint32_t u[kBytes / 4];
+  __device__ __forceinline__ void load(const char* p) {
+    if (kBytes == 16) {
+      load16<false>(u, p);
+    } else {
+      typedef u32x2 u32x2_any __attribute__((aligned(2)));
+      const u32x2 v = *reinterpret_cast<const u32x2_any*>(p);
+      __builtin_memcpy(u, &v, 8);
+    }
+  }
+  __device__ __forceinline__ void widen(float (&v)[N]) const {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (DT == SCAPE_F32) v[j] = __uint_as_float(u[j % (kBytes / 4)]);
+      else if (DT == SCAPE_BF16) v[j] = __uint_as_float((j & 1) ? u[j / 2] & 0xffff0000u : u[j / 2] << 16);
+      else v[j] = (float)__builtin_bit_cast(_Float16, (uint16_t)(u[j / 2] >> (16 * (j & 1))));
+    }
+  }
+};
+
+// Calls many(i, x) for N elements at a time where they lie wholly in [lo, hi),
+// DEEP of a thread's on the way, and one(i) for the elements behind them.
+template <int DT, int N, int DEEP, typename F, typename G>
+__device__ __forceinline__ void walk(const void* data, int64_t lo, int64_t hi, F many, G one) {
+  constexpr int kSize = DT == SCAPE_F32 ? 4 : 2;
+  const char* const base = static_cast<const char*>(data);
+  constexpr int64_t step = (int64_t)kThreads * N;
+  int64_t i = lo + (int64_t)threadIdx.x * N;
+  for (; lo + DEEP * step <= hi; lo += DEEP * step, i += DEEP * step) {
+    Some<DT, N> x[DEEP];
+#pragma unroll
+    for (int k = 0; k < DEEP; ++k) x[k].load(base + (i + k * step) * kSize);
+#pragma unroll
+    for (int k = 0; k < DEEP; ++k) many(i + k * step, x[k]);
+  }
+  for (; i + N <= hi; i += step) {
+    Some<DT, N> x;
+    x.load(base + i * kSize);
+    many(i, x);
+  }
+  for (int64_t j = i; j < hi; ++j) one(j);
 }
 
 template <int DT>
-__device__ __forceinline__ double squares(const Span& s, int64_t lo, int64_t hi) {
-  double sum = 0.0;
-  for (int64_t i = lo + (int64_t)threadIdx.x * 8; i < hi; i += kThreads * 8) {
-    float v[8];
-    load8<DT>(s.data, 0, i, hi, v);
+__device__ __forceinline__ double squares(const Piece& p) {
+  double sum[4] = {0.0, 0.0, 0.0, 0.0};
+  constexpr int N = DT == SCAPE_F32 ? 4 : 8;
+  walk<DT, N, 4>(
+      p.data, p.lo, p.hi,
+      [&](int64_t, const Some<DT, N>& x) {
+        float v[N];
+        x.widen(v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum = __builtin_fma((double)v[j], (double)v[j], sum);
-  }
-  return sum;
+        for (int j = 0; j < N; ++j) sum[j & 3] = __builtin_fma((double)v[j], (double)v[j], sum[j & 3]);
+      },
+      [&](int64_t i) {
+        const double x = Elem<DT>::get(p.data, i);
+        sum[0] = __builtin_fma(x, x, sum[0]);
+      });
+  return (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 
 __global__ void __launch_bounds__(kThreads) grad_sum_kernel(SpanArgs a) {
   __shared__ double lds[kThreads / 64];
-  const int32_t piece = a.span[0].first + (int32_t)blockIdx.x;
-  const Span s = a.span[span_of(a, piece)];
-  const int64_t lo = (piece - s.first) * a.piece;
-  const int64_t hi = lo + a.piece < s.count ? lo + a.piece : s.count;
+  const int32_t piece = a.begin + (int32_t)blockIdx.x;
+  const Piece p(a, piece);
   double sum;
-  if (s.dtype == SCAPE_F32) sum = squares<SCAPE_F32>(s, lo, hi);
-  else if (s.dtype == SCAPE_BF16) sum = squares<SCAPE_BF16>(s, lo, hi);
-  else sum = squares<SCAPE_F16>(s, lo, hi);
-  sum = block_sum(sum, lds);
+  if (p.dtype == SCAPE_F32) sum = squares<SCAPE_F32>(p);
+  else if (p.dtype == SCAPE_BF16) sum = squares<SCAPE_BF16>(p);
+  else sum = squares<SCAPE_F16>(p);
+  sum = block_sum<kThreads>(sum, lds);
   if (threadIdx.x == 0) a.sums[piece] = sum;
 }
 
 // One workgroup a group: its norm and the factor of its gradients.
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(GroupArgs a) {
-  __shared__ double lds[kThreads / 64];
+constexpr int kNormThreads = 1024;
+__global__ void __launch_bounds__(kNormThreads) grad_norm_kernel(GroupArgs a) {
+  __shared__ double lds[kNormThreads / 64];
   const int g = blockIdx.x;
-  double sum = 0.0;
-  for (int32_t i = a.first[g] + threadIdx.x; i < a.first[g + 1]; i += kThreads) sum += a.sums[i];
-  sum = block_sum(sum, lds);
+  const double sum = group_sum<kNormThreads>(a.sums + a.first[g], a.first[g + 1] - a.first[g], lds);
   if (threadIdx.x != 0) return;
-  const double norm = sqrt(sum) * (double)a.scale;
+  const double norm = sqrt(sum) * (double)a.s.scale;
   a.norm[g] = (float)norm;
-  if (!a.clip) return;
-  const bool over = norm > (double)a.max_norm && norm < (double)__builtin_inff();
-  a.factors[g] = over ? (double)a.scale * ((double)a.max_norm / norm) : (double)a.scale;
+  if (a.clip) a.factors[g] = factor_of(norm, a.s);
+}
+
+template <int DT, int OT, bool STREAM>
+__device__ __forceinline__ void scale_piece(const Piece& p, double f) {
+  // 16 bytes of the wider side a lane, so that neighbouring lanes' accesses
+  // join: bf16 to fp32 at 32 bytes a lane took 970 us where this takes 620
+  // (557 million elements)
+  constexpr int N = OT == SCAPE_F32 ? 4 : 8;
+  walk<DT, N, DT == OT ? 4 : 8>(
+      p.data, p.lo, p.hi,
+      [&](int64_t i, const Some<DT, N>& x) {
+        float v[N];
+        x.widen(v);
+        // one rounding: the product is exact in 64 bits, or next to it
+        typename Elem<OT>::T o[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) Elem<OT>::put(o, j, (float)((double)v[j] * f));
+        u32x4 w;
+        __builtin_memcpy(&w, o, 16);
+        u32x4_any* q = reinterpret_cast<u32x4_any*>(static_cast<typename Elem<OT>::T*>(p.out) + i);
+        if (STREAM) __builtin_nontemporal_store(w, q);
+        else *q = w;
+      },
+      [&](int64_t i) { Elem<OT>::put(p.out, i, (float)((double)Elem<DT>::get(p.data, i) * f)); });
 }
 
 template <int DT, int OT>
-__device__ __forceinline__ void scale_span(const Span& s, int64_t lo, int64_t hi, double f) {
-  for (int64_t i = lo + (int64_t)threadIdx.x * 8; i < hi; i += kThreads * 8) {
-    float v[8];
-    load8<DT>(s.data, 0, i, hi, v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = (float)((double)v[j] * f);
-    store8<OT>(s.out, 0, i, hi, v);
-  }
+__device__ __forceinline__ void scale_some(const Piece& p, double f, bool stream) {
+  if (stream) scale_piece<DT, OT, true>(p, f);
+  else scale_piece<DT, OT, false>(p, f);
 }
 
-__global__ void __launch_bounds__(kThreads) grad_scale_kernel(SpanArgs a) {
-  const int32_t piece = a.span[0].first + (int32_t)blockIdx.x;
-  const Span s = a.span[span_of(a, piece)];
-  const int64_t lo = (piece - s.first) * a.piece;
-  const int64_t hi = lo + a.piece < s.count ? lo + a.piece : s.count;
-  const double f = a.factors[s.group];
-  if (f == 1.0 && s.out == s.data) return;
-  if (s.dtype == SCAPE_F32) scale_span<SCAPE_F32, SCAPE_F32>(s, lo, hi, f);
-  else if (s.dtype == SCAPE_BF16 && s.out_dtype == SCAPE_BF16) scale_span<SCAPE_BF16, SCAPE_BF16>(s, lo, hi, f);
-  else if (s.dtype == SCAPE_BF16) scale_span<SCAPE_BF16, SCAPE_F32>(s, lo, hi, f);
-  else if (s.out_dtype == SCAPE_F16) scale_span<SCAPE_F16, SCAPE_F16>(s, lo, hi, f);
-  else scale_span<SCAPE_F16, SCAPE_F32>(s, lo, hi, f);
+__global__ void __launch_bounds__(kThreads) grad_scale_kernel(SpanArgs a, Scaling s) {
+  __shared__ double lds[kThreads / 64];
+  const int32_t piece = a.end - 1 - (int32_t)blockIdx.x;
+  const Piece p(a, piece);
+  double f;
+  if (s.factors) {
+    f = s.factors[p.group];
+  } else {
+    const int32_t first = p.group * s.group_pieces;
+    const double norm = sqrt(group_sum<kThreads>(a.sums + first, s.group_pieces, lds)) * (double)s.scale;
+    f = factor_of(norm, s);
+    if (piece == first && threadIdx.x == 0) s.norm[p.group] = (float)norm;
+  }
+  if (f == 1.0 && p.out == p.data) return;
+  if (p.dtype == SCAPE_F32) scale_some<SCAPE_F32, SCAPE_F32>(p, f, s.stream);
+  else if (p.dtype == SCAPE_BF16 && p.out_dtype == SCAPE_BF16) scale_some<SCAPE_BF16, SCAPE_BF16>(p, f, s.stream);
+  else if (p.dtype == SCAPE_BF16) scale_some<SCAPE_BF16, SCAPE_F32>(p, f, s.stream);
+  else if (p.out_dtype == SCAPE_F16) scale_some<SCAPE_F16, SCAPE_F16>(p, f, s.stream);
+  else scale_some<SCAPE_F16, SCAPE_F32>(p, f, s.stream);
 }
 
 // Elements of a piece (a multiple of what a workgroup reads at a time), so
@@ -158,53 +273,69 @@ hipError_t launch_grads(int32_t count, const scape_grad* grads, int32_t groups, 
   const int32_t per = count / groups;
   double* sums = static_cast<double*>(ws);
   double* factors = sums + pieces_of(count, grads);
+  int64_t bytes = 0;
+  for (int32_t i = 0; i < count; ++i)
+    bytes += grads[i].count * (int64_t)(dtype_bytes(grads[i].dtype) +
+                                        (grads[i].out ? dtype_bytes(grads[i].out_dtype) : 0));
+
+  // groups of as many pieces each, and few: one launch less
+  int64_t each = 0;
+  bool alike = clip;
+  for (int32_t g = 0; alike && g < groups; ++g) {
+    int64_t n = 0;
+    for (int32_t i = g * per; i < (g + 1) * per; ++i) n += pieces(grads[i].count, piece);
+    if (g == 0) each = n;
+    alike = n == each && n > 0 && n <= kFewPieces;
+  }
+  const Scaling how{alike ? nullptr : factors, norm, scale, max_norm, (int32_t)each, bytes > kStreamBytes};
 
   const auto walk = [&](bool scaling) {
     SpanArgs a;
     a.piece = piece;
     a.sums = sums;
-    a.factors = factors;
-    a.n = 0;
-    int32_t at = 0;
+    int32_t at = 0, n = 0;
     for (int32_t i = 0; i <= count; ++i) {
-      if (a.n > 0 && (i == count || a.n == kSpans)) {
+      const bool far = n > 0 && i < count && i / per - a.group >= kLaunchGroups;
+      if (n > 0 && (i == count || n == kSpans || far)) {
+        a.begin = a.first[0];
         a.end = at;
-        const dim3 grid((unsigned)(at - a.span[0].first));
-        if (scaling) grad_scale_kernel<<<grid, kThreads, 0, s>>>(a);
+        for (int32_t j = n; j < kSpans; ++j) a.first[j] = INT32_MAX;
+        const dim3 grid((unsigned)(a.end - a.begin));
+        if (scaling) grad_scale_kernel<<<grid, kThreads, 0, s>>>(a, how);
         else grad_sum_kernel<<<grid, kThreads, 0, s>>>(a);
-        a.n = 0;
+        n = 0;
       }
       if (i == count || grads[i].count == 0) continue;
       const scape_grad& g = grads[i];
-      Span& p = a.span[a.n++];
+      if (n == 0) a.group = i / per;
+      a.first[n] = at;
+      Span& p = a.span[n++];
       p.data = g.data;
       p.out = g.out ? g.out : const_cast<void*>(g.data);
-      p.count = g.count;
-      p.first = at;
-      p.dtype = (int16_t)g.dtype;
-      p.out_dtype = (int16_t)(g.out ? g.out_dtype : g.dtype);
-      p.group = i / per;
+      p.what = (uint64_t)g.count | (uint64_t)g.dtype << 48 | (uint64_t)(g.out ? g.out_dtype : g.dtype) << 50 |
+               (uint64_t)(i / per - a.group) << 52;
       at += (int32_t)pieces(g.count, piece);
     }
   };
 
   walk(false);
-  GroupArgs b;
-  b.scale = scale;
-  b.max_norm = max_norm;
-  b.clip = clip;
-  b.sums = sums;
-  int32_t at = 0;
-  for (int32_t g0 = 0; g0 < groups; g0 += kSpans) {
-    b.n = groups - g0 < kSpans ? groups - g0 : kSpans;
-    for (int32_t g = 0; g < b.n; ++g) {
-      b.first[g] = at;
-      for (int32_t i = (g0 + g) * per; i < (g0 + g + 1) * per; ++i) at += (int32_t)pieces(grads[i].count, piece);
+  if (!alike) {
+    GroupArgs b;
+    b.s = how;
+    b.clip = clip;
+    b.sums = sums;
+    int32_t at = 0;
+    for (int32_t g0 = 0; g0 < groups; g0 += kSpans) {
+      const int32_t n = groups - g0 < kSpans ? groups - g0 : kSpans;
+      for (int32_t g = 0; g < n; ++g) {
+        b.first[g] = at;
+        for (int32_t i = (g0 + g) * per; i < (g0 + g + 1) * per; ++i) at += (int32_t)pieces(grads[i].count, piece);
+      }
+      b.first[n] = at;
+      b.factors = factors + g0;
+      b.norm = norm + g0;
+      grad_norm_kernel<<<dim3((unsigned)n), kNormThreads, 0, s>>>(b);
     }
-    b.first[b.n] = at;
-    b.factors = factors + g0;
-    b.norm = norm + g0;
-    grad_norm_kernel<<<dim3((unsigned)b.n), kThreads, 0, s>>>(b);
   }
   if (clip) walk(true);
   return hipGetLastError();

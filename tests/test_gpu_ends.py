@@ -559,6 +559,17 @@ def test_clip_long_and_many(S):
     S.grad_norm(gl, n, scratch(S.grad_workspace_bytes(gl)))
     want = [E.grad_norm([f64(grads[2 * i]), f64(grads[2 * i + 1])]) for i in range(350)]
     within(n, np.array(want), np.array(want) * U * (1 + 1e-6), "norms")
+    # groups far apart in one launch: all but a few tensors are empty
+    some = {3: 2.0, 4100: 3.0, 9000: 5.0}
+    grads = [torch.full((2,) if i in some else (0,), some.get(i, 0.0), device=DEV) for i in range(10000)]
+    gl = S.GradList(grads, groups=10000)
+    n = torch.full((10000,), -1.0, device=DEV)
+    S.clip_grads(gl, 1.0, n, scratch(S.grad_workspace_bytes(gl)))
+    want = torch.zeros(10000, dtype=torch.float64)
+    for i, v in some.items():
+        want[i] = v * 2 ** 0.5
+        assert (grads[i] - 2 ** -0.5).abs().max() < 1e-7
+    within(n, want.numpy(), want.numpy() * U * (1 + 1e-6), "norms")
 
 
 def test_optimizer_clips_each_worker(S):
