@@ -17,25 +17,25 @@ struct EmbedArgs {
 };
 
 // out[t] = scale * table[ids[t]] + pos_table[pos[t]]: one read and one write,
-// bound by memory.
+// bound by memory.  `lanes` (a power of two) threads share a token.
 template <int TT, int OT>
-__global__ void __launch_bounds__(kThreads) embed_kernel(EmbedArgs a) {
-  const int64_t chunks = (a.cols + 7) / 8;
-  for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+__global__ void __launch_bounds__(kThreads) embed_kernel(EmbedArgs a, int lanes) {
+  const int per = kThreads / lanes;
+  for (int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / lanes; t < a.tokens; t += (int64_t)gridDim.x * per) {
     const int64_t id = token_at(a.ids, t);
     const int64_t at = a.pos_table ? token_at(a.pos, t) : -1;
-    for (int64_t i = threadIdx.x; i < chunks; i += kThreads) {
+    for (int64_t c = (threadIdx.x & (lanes - 1)) * 8; c < a.cols; c += lanes * 8) {
       float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (id >= 0 && id < a.vocab) load8<TT>(a.table, id * a.table_ld, i * 8, a.cols, v);
+      if (id >= 0 && id < a.vocab) load8<TT>(a.table, id * a.table_ld, c, a.cols, v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] *= a.scale;
       if (at >= 0 && at < a.positions) {
         float p[8];
-        load8<TT>(a.pos_table, at * a.pos_ld, i * 8, a.cols, p);
+        load8<TT>(a.pos_table, at * a.pos_ld, c, a.cols, p);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] += p[j];
       }
-      store8<OT>(a.out, t * a.out_ld, i * 8, a.cols, v);
+      store8<OT>(a.out, t * a.out_ld, c, a.cols, v);
     }
   }
 }
@@ -111,12 +111,14 @@ __global__ void __launch_bounds__(kThreads) embed_sort_kernel(SortArgs a) {
 // words and goes through all tokens.  Its waves take a stretch of them each,
 // list those of the slab in LDS and count them by word; a token's place is the
 // number of tokens of lower words, of the same word in the stretches before,
-// and of the same word before it in its list.
+// and of the same word before it in its own.  Where the lists have no room for
+// all tokens, the waves go through their stretch a second time instead.
 constexpr int kSlabThreads = 1024;
 constexpr int kSlabWaves = kSlabThreads / 64;
 constexpr int kSlabMax = 512;
-constexpr int64_t kSlabTokens = 16384;  // the lists' room
-constexpr int64_t kSlabs = 1024;        // workgroups at most: each goes through all tokens
+constexpr int64_t kListTokens = 16384;             // the lists' room
+constexpr int64_t kSlabs = 1024;                   // workgroups at most: each goes through all tokens
+constexpr int64_t kSlabWork = int64_t(1) << 28;    // tokens that they go through in all, at most
 constexpr int kAhead = 8;               // tokens of a lane on the way at a time
 
 struct SlabArgs {
@@ -136,7 +138,7 @@ __device__ __forceinline__ uint32_t lanes_below(uint64_t mask) {
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
 }
 
-template <typename I>
+template <typename I, bool LIST>
 __global__ void __launch_bounds__(kSlabThreads) embed_slab_kernel(SlabArgs a) {
   extern __shared__ uint32_t lds[];  // [kSlabWaves][slab] counts, then places; [kSlabWaves][stretch] lists
   __shared__ uint32_t first[kSlabThreads], wave_lower[kSlabWaves], wave_total[kSlabWaves];
@@ -150,34 +152,39 @@ __global__ void __launch_bounds__(kSlabThreads) embed_slab_kernel(SlabArgs a) {
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 
-  const int from = wave * a.stretch;
-  const int left = (int)a.tokens - from;
-  const int own = left < a.stretch ? left : a.stretch;  // not positive: none
+  const int64_t from = (int64_t)wave * a.stretch;
+  const int64_t left = a.tokens - from;
+  const int own = (int)(left < a.stretch ? left : a.stretch);  // not positive: none
   const I* const ids = static_cast<const I*>(a.ids) + from;
-  uint32_t lower = 0, listed = 0;
-  for (int t0 = lane; t0 - lane < own; t0 += 64 * kAhead) {
-    I id[kAhead];
+  // Calls f(word, place in the stretch) for the stretch, 64 tokens at a time.
+  const auto walk = [&](auto f) {
+    for (int t0 = lane; t0 - lane < own; t0 += 64 * kAhead) {
+      I id[kAhead];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int t = t0 + j * 64;
-      id[j] = ids[t < own ? t : own - 1];
-    }
+      for (int j = 0; j < kAhead; ++j) {
+        const int t = t0 + j * 64;
+        id[j] = ids[t < own ? t : own - 1];
+      }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int t = t0 + j * 64;
-      const uint32_t w = t < own ? word_of(id[j]) : kNoWord;
-      const uint32_t r = w - lo;
-      lower += w < lo ? 1 : 0;
-      const uint64_t in = __ballot(r < words);
-      if (in) {
-        if (r < words) {
-          list[listed + lanes_below(in)] = r << 16 | (uint32_t)t;
-          atomicAdd(&mine[r], 1u);  // of LDS; a sum of ones has no order
-        }
-        listed += (uint32_t)__popcll(in);
+      for (int j = 0; j < kAhead; ++j) {
+        const int t = t0 + j * 64;
+        f(t < own ? word_of(id[j]) : kNoWord, t);
       }
     }
-  }
+  };
+  uint32_t lower = 0, listed = 0;
+  walk([&](uint32_t w, int t) {
+    const uint32_t r = w - lo;
+    lower += w < lo ? 1 : 0;
+    const uint64_t in = __ballot(r < words);
+    if (in) {
+      if (r < words) {
+        if (LIST) list[listed + lanes_below(in)] = r << 16 | (uint32_t)t;
+        atomicAdd(&mine[r], 1u);  // of LDS; a sum of ones has no order
+      }
+      listed += (uint32_t)__popcll(in);
+    }
+  });
   lower = wave_sum(lower);
   if (lane == 0) wave_lower[wave] = lower;
   __syncthreads();
@@ -206,24 +213,30 @@ __global__ void __launch_bounds__(kSlabThreads) embed_slab_kernel(SlabArgs a) {
   first[threadIdx.x] = base + scan - sum;
   __syncthreads();
 
-  for (uint32_t i0 = 0; i0 < listed; i0 += 64) {
-    const bool there = i0 + lane < listed;
-    const uint32_t e = there ? list[i0 + lane] : 0xffffffffu;
-    const uint32_t r = e >> 16;
-    for (uint64_t open = __ballot(there); open;) {
+  // Places up to 64 tokens of the slab in their order; r: none of its words.
+  const auto place = [&](uint32_t r, uint32_t t) {
+    for (uint64_t open = __ballot(r < words); open;) {
       const uint32_t x = (uint32_t)__builtin_amdgcn_readlane((int)r, __builtin_ctzll(open));
-      const uint64_t same = __ballot(r == x);  // no slab has a word 0xffff
+      const uint64_t same = __ballot(r == x);
       open &= ~same;
       const uint32_t at = first[x] + mine[x] + lanes_below(same);
       if (r == x) {
         a.word[at] = lo + x;
-        a.token[at] = (uint32_t)from + (e & 0xffffu);
+        a.token[at] = t;
       }
       if (lane == 0) mine[x] += (uint32_t)__popcll(same);
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     }
+  };
+  if (LIST) {
+    for (uint32_t i0 = 0; i0 < listed; i0 += 64) {
+      const uint32_t e = i0 + lane < listed ? list[i0 + lane] : 0xffffffffu;
+      place(e >> 16, (uint32_t)from + (e & 0xffffu));
+    }
+  } else if (listed) {
+    walk([&](uint32_t w, int t) { place(w - lo, (uint32_t)from + (uint32_t)t); });
   }
   if (blockIdx.x == gridDim.x - 1)  // the places behind the last word's
     for (int64_t i = end + threadIdx.x; i < a.padded; i += kSlabThreads) {
@@ -409,53 +422,84 @@ __global__ void __launch_bounds__(kThreads) embed_chunk_kernel(ChunkArgs a) {
   if (cur != kNoWord) flush(true);
 }
 
-// Joins the sums of a word that crosses chunks, in the chunk k where it begins:
-// four waves add a quarter of its partial rows each, in order, then the
-// quarters.  A lane owns 4 columns.
-__device__ __forceinline__ void join_word(const ChunkArgs& a, int32_t k, f32x4 (*lds)[64]) {
+// Partial rows of the word that crosses from chunk k into the next and begins
+// in k: k's last, then the first of each chunk that begins with it.  0: none.
+__device__ __forceinline__ int64_t partial_rows(const ChunkArgs& a, int32_t k, uint32_t* word) {
   const int64_t p0 = (int64_t)k * a.chunk, p1 = p0 + a.chunk;
   const uint32_t w = a.word[p1 - 1], after = a.word[p1], first = a.word[p0];
   const uint32_t before = a.word[p0 > 0 ? p0 - 1 : 0];
   const auto begin_of = [&](int64_t chunk) { return chunk < a.chunks ? a.word[chunk * a.chunk] : kNoWord; };
   uint32_t begins = begin_of(k + 1 + (threadIdx.x & 63));
-  if (w == kNoWord || after != w) return;
-  if (first == w && p0 > 0 && before == w) return;  // begins further ahead
-  // partial rows: k's last, then the first of each chunk that begins with the word
+  *word = w;
+  if (w == kNoWord || after != w) return 0;
+  if (first == w && p0 > 0 && before == w) return 0;  // begins further ahead
   int64_t n = 1;
   for (int64_t at = k + 1;;) {
     const uint64_t others = __ballot(begins != w);
     n += others ? __builtin_ctzll(others) : 64;
-    if (others) break;
+    if (others) return n;
     at += 64;
     begins = begin_of(at + (threadIdx.x & 63));
   }
-  const int q = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t c = ((int64_t)blockIdx.y * 64 + lane) * 4;
-  const bool mine = c < a.pitch;
-  const int64_t from = n * q / 4, to = n * (q + 1) / 4;
+}
+
+// The sum of partial rows [from, to) of chunk k's word at columns [c, c + 4).
+__device__ __forceinline__ f32x4 part_sum(const ChunkArgs& a, int32_t k, int64_t from, int64_t to, int64_t c) {
   f32x4 sum = {0, 0, 0, 0};
-  if (mine) {
 #pragma unroll 8
-    for (int64_t i = from; i < to; ++i) {
-      const float* p = a.part + ((k + i) * 2 + (i == 0 ? 1 : 0)) * a.pitch + c;
-      sum += *reinterpret_cast<const f32x4*>(p);
-    }
+  for (int64_t i = from; i < to; ++i) {
+    const float* p = a.part + ((k + i) * 2 + (i == 0 ? 1 : 0)) * a.pitch + c;
+    sum += *reinterpret_cast<const f32x4*>(p);
   }
-  __syncthreads();  // the sums of the word before have been read
-  if (q > 0) lds[q - 1][lane] = sum;
-  __syncthreads();
-  if (q > 0 || !mine) return;
-  sum = ((sum + lds[0][lane]) + lds[1][lane]) + lds[2][lane];
+  return sum;
+}
+
+__device__ __forceinline__ void put_sum(const ChunkArgs& a, uint32_t w, int64_t c, f32x4 sum) {
   float* row = a.dtable + (int64_t)w * a.cols;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if (c + j < a.cols) row[c + j] = a.accumulate ? __builtin_fmaf(a.scale, sum[j], row[c + j]) : a.scale * sum[j];
 }
 
+// Joins the sums of words that cross chunks: a wave a chunk, 4 columns a lane.
+// Where a word has many partial rows the four waves add a quarter of them each,
+// in order, then the quarters.
+constexpr int kLongJoin = 16;
 __global__ void __launch_bounds__(kThreads) embed_join_kernel(ChunkArgs a) {
   __shared__ f32x4 lds[3][64];
-  for (int32_t k = blockIdx.x; k + 1 < a.chunks; k += gridDim.x) join_word(a, k, lds);
+  __shared__ int64_t rows[4];
+  __shared__ uint32_t words[4];
+  const int q = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int64_t c = ((int64_t)blockIdx.y * 64 + lane) * 4;
+  const bool mine = c < a.pitch;
+  for (int64_t k0 = (int64_t)blockIdx.x * 4; k0 + 1 < a.chunks; k0 += (int64_t)gridDim.x * 4) {
+    const int32_t k = (int32_t)k0 + q;
+    uint32_t w = kNoWord;
+    const int64_t n = k + 1 < a.chunks ? partial_rows(a, k, &w) : 0;
+    if (n > 0 && n <= kLongJoin && mine) put_sum(a, w, c, part_sum(a, k, 0, n, c));
+    if (lane == 0) {
+      rows[q] = n > kLongJoin ? n : 0;
+      words[q] = w;
+    }
+    __syncthreads();
+    for (int b = 0; b < 4; ++b) {
+      const int64_t m = rows[b];
+      if (m == 0) continue;
+      const f32x4 sum = mine ? part_sum(a, (int32_t)k0 + b, m * q / 4, m * (q + 1) / 4, c) : f32x4{0, 0, 0, 0};
+      if (q > 0) lds[q - 1][lane] = sum;
+      __syncthreads();
+      if (q == 0 && mine) put_sum(a, words[b], c, ((sum + lds[0][lane]) + lds[1][lane]) + lds[2][lane]);
+      __syncthreads();
+    }
+    __syncthreads();  // rows and words have been read
+  }
 }
+
+// Rows of no token are cleared past the caches where the table and dy together
+// are more than they hold.  Table of 32000 x 2048 (250 MiB), with the forward
+// pass, past the caches and through them: 16384 tokens 95 and 116 us, 4096
+// tokens 72 and 70, 64 tokens 60 and 49; 50257 x 1024, 8192 tokens: 103 and 89.
+constexpr int64_t kClearStream = int64_t(288) << 20;
 
 // How a gradient's tokens are cut, and its workspace.
 struct BackPlan {
@@ -479,7 +523,7 @@ BackPlan back_plan(int64_t tokens, int64_t cols) {
   p.pitch = eights * 8;
   // long chunks write few partial rows, short ones fill the card
   p.chunk = 32;
-  while (p.chunk > 8 && p.padded / p.chunk * p.slabs * p.lanes < 2048 * 64) p.chunk /= 2;
+  while (p.chunk > 8 && p.padded / p.chunk * p.slabs * p.lanes < 1024 * 64) p.chunk /= 2;
   p.chunks = (int32_t)(p.padded / p.chunk);
   size_t at = 0;
   const auto take = [&](size_t n) {
@@ -506,20 +550,23 @@ void launch_chunks(const ChunkArgs& a, dim3 grid, hipStream_t s) {
 
 template <int TT>
 void embed_out(const EmbedArgs& a, int out, hipStream_t s) {
-  const dim3 grid(capped(a.tokens, 1 << 20));
-  if (out == SCAPE_F32) embed_kernel<TT, SCAPE_F32><<<grid, kThreads, 0, s>>>(a);
-  else if (out == SCAPE_BF16) embed_kernel<TT, SCAPE_BF16><<<grid, kThreads, 0, s>>>(a);
-  else embed_kernel<TT, SCAPE_F16><<<grid, kThreads, 0, s>>>(a);
+  int lanes = 1;
+  while (lanes < kThreads && lanes * 8 < a.cols) lanes *= 2;
+  const dim3 grid(capped((a.tokens * lanes + kThreads - 1) / kThreads, 1 << 20));
+  if (out == SCAPE_F32) embed_kernel<TT, SCAPE_F32><<<grid, kThreads, 0, s>>>(a, lanes);
+  else if (out == SCAPE_BF16) embed_kernel<TT, SCAPE_BF16><<<grid, kThreads, 0, s>>>(a, lanes);
+  else embed_kernel<TT, SCAPE_F16><<<grid, kThreads, 0, s>>>(a, lanes);
 }
 
 // Words that a workgroup of the slab sort owns: about one workgroup a CU.  0:
-// sorted by tiles.  16384 tokens of 32000 words: slabs 7.5 us, tiles and their
-// merge 16.5; 1531 of 4099: 5.2 against 10.5.  The lists of more tokens do not
-// fit LDS, and more slabs than kSlabs would go through the tokens too often.
+// sorted by tiles, which can be any number.  16384 tokens of 32000 words: slabs
+// 7.5 us, tiles and their merge 16.5; 1531 of 4099: 5.2 against 10.5; 65536 of
+// 32000 x 1024, all of the call: 184 against 222.
 int slab_of(int64_t tokens, int64_t vocab) {
   int slab = 4;
   while (slab < kSlabMax && (vocab + slab - 1) / slab > 256) slab *= 2;
-  return tokens <= kSlabTokens && (vocab + slab - 1) / slab <= kSlabs ? slab : 0;
+  const int64_t slabs = (vocab + slab - 1) / slab;
+  return slabs <= kSlabs && tokens * slabs <= kSlabWork ? slab : 0;
 }
 
 // Sorts tiles and merges them; which pair of buffers holds the result.
@@ -570,9 +617,11 @@ hipError_t launch_embed_backward(int64_t tokens, int64_t vocab, int64_t cols, co
     const int stretch = (int)((tokens + kSlabThreads - 1) / kSlabThreads) * 64;
     const SlabArgs a{tokens, vocab, p.padded, ids.data, slab, stretch, at(p.word[0]), at(p.token[0])};
     const dim3 grid((unsigned)((vocab + slab - 1) / slab));
-    const size_t lds = (size_t)(slab + stretch) * kSlabWaves * 4;
-    if (ids.bits == 64) embed_slab_kernel<int64_t><<<grid, kSlabThreads, lds, s>>>(a);
-    else embed_slab_kernel<int32_t><<<grid, kSlabThreads, lds, s>>>(a);
+    const bool list = tokens <= kListTokens;
+    const size_t lds = (size_t)(slab + (list ? stretch : 0)) * kSlabWaves * 4;
+    const auto go = [&](auto kernel) { kernel<<<grid, kSlabThreads, lds, s>>>(a); };
+    if (ids.bits == 64) go(list ? embed_slab_kernel<int64_t, true> : embed_slab_kernel<int64_t, false>);
+    else go(list ? embed_slab_kernel<int32_t, true> : embed_slab_kernel<int32_t, false>);
   } else if (tokens > 0) {
     from = sort_tiles(p, tokens, vocab, ids, base, s);
   }
@@ -584,13 +633,14 @@ hipError_t launch_embed_backward(int64_t tokens, int64_t vocab, int64_t cols, co
   const int64_t clearing = accumulate ? 0 : (vocab + 4 * rows - 1) / (4 * rows);
   const ChunkArgs ca{cols, at(p.word[from]), at(p.token[from]), p.chunk, p.chunks, p.lanes, p.slabs, dy.data, dy.ld,
                      scale, dtable, accumulate, reinterpret_cast<float*>(base + p.part), p.pitch, blocks, vocab,
-                     (int)rows, vocab * cols * 4 > kStreamBytes};
+                     (int)rows, (vocab * 4 + tokens * (int64_t)dtype_bytes(dy.dtype)) * cols > kClearStream};
   const dim3 grid((unsigned)(blocks + clearing));
   if (dy.dtype == SCAPE_F32) launch_chunks<SCAPE_F32>(ca, grid, s);
   else if (dy.dtype == SCAPE_BF16) launch_chunks<SCAPE_BF16>(ca, grid, s);
   else launch_chunks<SCAPE_F16>(ca, grid, s);
   if (p.chunks > 1)
-    embed_join_kernel<<<dim3(capped(p.chunks - 1, 1 << 20), (unsigned)((p.pitch + 255) / 256)), kThreads, 0, s>>>(ca);
+    embed_join_kernel<<<dim3(capped((p.chunks + 2) / 4, 1 << 20), (unsigned)((p.pitch + 255) / 256)), kThreads, 0, s>>>(
+        ca);
   return hipGetLastError();
 }
 

@@ -239,8 +239,10 @@ struct Row : Cut<DT> {
     for (int i = 0; i < C; ++i) {
       float v[N];
       r[i].keep();
-      r[i].unpack(v);
-      f(Cut<DT>::chunk(index(i)), Number<N>{}, v);
+      if (i * T < whole) {  // of some thread
+        r[i].unpack(v);
+        f(Cut<DT>::chunk(index(i)), Number<N>{}, v);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
     f(Cut<DT>::single(Team<T>::thread()), Number<1>{}, &one);
@@ -511,13 +513,13 @@ __device__ __forceinline__ void put_row(const LogprobArgs& a, int64_t r, R& row,
   }
 }
 
-template <int DT, int T, bool ENT, typename R>
+template <int DT, int T, bool ENT, bool STREAM, typename R>
 __device__ __forceinline__ void put_gradient(const LogprobArgs& a, int64_t r, R& row, const RowResult& x,
                                              const RowLds<T>& l) {
   const RowGradient g(a, r, x.m, x.ls, x.h);
   char* const out = static_cast<char*>(a.dlogits.data) + r * a.dlogits.ld * Chunk<DT>::kSize;
   row.each([&](int first, auto n, float* v) {
-    emit_some<DT, ENT, false>(g, out, first, n, n > 1 ? row.chunks_end() : row.vocab, v);
+    emit_some<DT, ENT, STREAM>(g, out, first, n, n > 1 ? row.chunks_end() : row.vocab, v);
   });
   // by the thread that wrote its place before
   if (g.none || g.y < 0) return;
@@ -542,7 +544,9 @@ __device__ __forceinline__ int64_t load_target(const LogprobArgs& a, int64_t r, 
   return y;
 }
 
-// With the row in registers.
+// With the row in registers.  (Alternatives take the registers of a second
+// workgroup of a CU: forced into half, 2097 x 32001 bf16 with 20 of them takes 69
+// us instead of 83, but one row 11.2 instead of 9.6.)
 template <int DT, int T, int C, bool ENT, bool TOP>
 __global__ void __launch_bounds__(T == 64 ? 256 : T) logprobs_kernel(LogprobArgs a, int64_t r0) {
   __shared__ RowLds<T> all[Team<T>::kRows];
@@ -587,7 +591,7 @@ __global__ void __launch_bounds__(T == 64 ? 256 : T) logprobs_kernel(LogprobArgs
   const RowResult x(m, m == neg_inf() ? s[0] : s[0] + (s[2] - 1.0f), s[1], s[0] != s[0]);
   const Row<DT, T, 0> memory(in, a.vocab);
   put_row<DT, T, TOP>(a, r, row, memory, x, y, most, l);
-  if (a.dlogits.data) put_gradient<DT, T, ENT>(a, r, row, x, l);
+  if (a.dlogits.data) put_gradient<DT, T, ENT, false>(a, r, row, x, l);
 }
 
 // With the row passing by: sums relative to the thread's maximum so far, joined
@@ -680,18 +684,20 @@ __global__ void __launch_bounds__(T) logprobs_online_kernel(LogprobArgs a, int64
   }
   const RowResult x(m, o, sum[1], nan);
   put_row<DT, T, TOP>(a, r, row, row, x, y, mine, l);
-  if (a.dlogits.data) put_gradient<DT, T, ENT>(a, r, row, x, l);
+  if (a.dlogits.data) put_gradient<DT, T, ENT, true>(a, r, row, x, l);
 }
 
-// The gradient alone: a workgroup takes kBackChunks chunks a thread of one row.
+// The gradient alone: T threads take kBackChunks chunks each of one row.
 constexpr int kBackChunks = 4;
-template <int DT, bool STREAM>
+template <int DT, int T, bool STREAM>
 __global__ void __launch_bounds__(kThreads) logprobs_back_kernel(LogprobArgs a, int64_t pieces) {
   const int64_t count = a.rows * pieces;
-  for (int64_t k = blockIdx.x; k < count; k += gridDim.x) {
+  constexpr int kTeams = kThreads / T;
+  const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / T);
+  for (int64_t k = (int64_t)blockIdx.x * kTeams + team; k < count; k += (int64_t)gridDim.x * kTeams) {
     const int64_t i = count - 1 - k;  // the last rows, which the first call read last, are in the caches
     const int64_t r = i / pieces;
-    const int i0 = (int)(i - r * pieces) * (kBackChunks * kThreads) + threadIdx.x;
+    const int i0 = (int)(i - r * pieces) * (kBackChunks * T) + threadIdx.x % T;
     const RowGradient g(a, r, a.stats[2 * r], a.stats[2 * r + 1], a.dentropy ? a.entropy[r] : 0.0f);
     const char* const in = static_cast<const char*>(a.logits.data) + r * a.logits.ld * Chunk<DT>::kSize;
     char* const out = static_cast<char*>(a.dlogits.data) + r * a.dlogits.ld * Chunk<DT>::kSize;
@@ -699,20 +705,19 @@ __global__ void __launch_bounds__(kThreads) logprobs_back_kernel(LogprobArgs a, 
     const Cut<DT> row(in, a.vocab);
     // in logits' place the target's is read before its chunk is written, by the same thread
     const int unit = row.unit_of(g.y);
-    const bool mine = !g.none && g.y >= 0 && unit >= i0 && (unit - i0) % kThreads == 0 &&
-                      unit - i0 < kBackChunks * kThreads;
+    const bool mine = !g.none && g.y >= 0 && unit >= i0 && (unit - i0) % T == 0 && unit - i0 < kBackChunks * T;
     const float target = mine ? Elem<DT>::get(in, g.y) : 0.0f;
     const auto emit = [&](auto with_entropy) {
       constexpr bool ent = decltype(with_entropy)::value;
       Chunk<DT> x[kBackChunks];
 #pragma unroll
       for (int k = 0; k < kBackChunks; ++k) {
-        const int n = i0 + k * kThreads;
+        const int n = i0 + k * T;
         if (row.whole > 0) row.load(x[k], n);
       }
 #pragma unroll
       for (int k = 0; k < kBackChunks; ++k) {
-        const int n = i0 + k * kThreads;  // a chunk, or behind them a single logit
+        const int n = i0 + k * T;  // a chunk, or behind them a single logit
         float v[N];
         if (n < row.whole) {
           x[k].unpack(v);
@@ -758,20 +763,34 @@ void run(const LogprobArgs& a, hipStream_t s) {
 template <int DT>
 void run_type(const LogprobArgs& a, hipStream_t s) {
   const int64_t v = a.vocab;
+  // As few threads a row as hold it in 16 registers each (32 for fp32, and for
+  // 16 bits past 32768 logits), so that a CU has two rows or more.  Longer rows
+  // pass by: 1335 x 50257 fp32 49 us, in 64 registers 65; 1023 x 65537 bf16 34
+  // against 42; with the gradient 65 against 69, though they are read twice.
   constexpr int W = DT == SCAPE_F32 ? 2 : 1;  // chunks of 8 logits
   if (v <= 64 * 8) run<DT, 64, W>(a, s);
   else if (v <= 64 * 32) run<DT, 64, 4 * W>(a, s);
   else if (v <= 256 * 32) run<DT, 256, 4 * W>(a, s);
+  else if (v <= 512 * 32) run<DT, 512, 4 * W>(a, s);
   else if (v <= 1024 * 32) run<DT, 1024, 4 * W>(a, s);
-  else if (v <= 1024 * 64) run<DT, 1024, 8 * W>(a, s);
-  else if (W == 1 && v <= 1024 * 128) run<DT, 1024, W == 1 ? 16 : 0>(a, s);
+  else if (W == 1 && v <= 1024 * 64) run<DT, 1024, W == 1 ? 8 : 0>(a, s);
   else run<DT, 1024, 0>(a, s);
 }
 
+template <int DT, int T>
+void run_back(const LogprobArgs& a, bool stream, hipStream_t s) {
+  constexpr int N = Chunk<DT>::N;
+  const int64_t units = a.vocab / N + 2 * N;  // chunks and single logits, at most
+  const int64_t pieces = (units + kBackChunks * T - 1) / (kBackChunks * T);
+  const dim3 grid(capped((a.rows * pieces + kThreads / T - 1) / (kThreads / T)));
+  if (stream) logprobs_back_kernel<DT, T, true><<<grid, kThreads, 0, s>>>(a, pieces);
+  else logprobs_back_kernel<DT, T, false><<<grid, kThreads, 0, s>>>(a, pieces);
+}
+
 template <int DT>
-void run_back(const LogprobArgs& a, dim3 grid, int64_t pieces, bool stream, hipStream_t s) {
-  if (stream) logprobs_back_kernel<DT, true><<<grid, kThreads, 0, s>>>(a, pieces);
-  else logprobs_back_kernel<DT, false><<<grid, kThreads, 0, s>>>(a, pieces);
+void run_back(const LogprobArgs& a, bool stream, hipStream_t s) {
+  if (a.vocab <= 64 * 16) run_back<DT, 64>(a, stream, s);  // a wave a row
+  else run_back<DT, kThreads>(a, stream, s);
 }
 
 }  // namespace
@@ -788,17 +807,13 @@ hipError_t launch_logprobs(const LogprobArgs& a, void*, hipStream_t s) {
 
 hipError_t launch_logprobs_backward(const LogprobArgs& a, hipStream_t s) {
   if (a.rows == 0) return hipSuccess;
-  const int64_t n = a.logits.dtype == SCAPE_F32 ? 4 : 8;
-  const int64_t units = a.vocab / n + 2 * n;  // chunks and single logits, at most
-  const int64_t pieces = (units + kBackChunks * kThreads - 1) / (kBackChunks * kThreads);
-  const dim3 grid(capped(a.rows * pieces));
   // What the first call read is still in the caches: past them, dlogits does
   // not drive it out.  1999 x 32000 fp32, both calls: 121 us, without it 152.
   // (Not so in the call that does both: 8192 x 32000 bf16 191 us, with it 197.)
   const bool stream = 2 * a.rows * a.vocab * (int64_t)dtype_bytes(a.logits.dtype) > kStreamBytes;
-  if (a.logits.dtype == SCAPE_F32) run_back<SCAPE_F32>(a, grid, pieces, stream, s);
-  else if (a.logits.dtype == SCAPE_BF16) run_back<SCAPE_BF16>(a, grid, pieces, stream, s);
-  else run_back<SCAPE_F16>(a, grid, pieces, stream, s);
+  if (a.logits.dtype == SCAPE_F32) run_back<SCAPE_F32>(a, stream, s);
+  else if (a.logits.dtype == SCAPE_BF16) run_back<SCAPE_BF16>(a, stream, s);
+  else run_back<SCAPE_F16>(a, stream, s);
   return hipGetLastError();
 }
 

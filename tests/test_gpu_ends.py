@@ -181,7 +181,9 @@ def test_embed_backward_one_word(S, tokens):
 
 @pytest.mark.parametrize("tokens,vocab,cols", [(30000, 200, 96), (70000, 60000, 16), (9000, 40, 520),
                                                (131073, 3000, 24), (300000, 70, 8), (70000, 65536, 16),
-                                               (300000, 20000, 8), (600, 1 << 24, 1), (5000, 300000, 40), (16384, 500000, 8), (16385, 9, 8)])
+                                               (300000, 20000, 8), (600, 1 << 24, 1), (5000, 300000, 40), (16384, 500000, 8),
+                                               (16385, 9, 8), (3000, 1 << 22, 2), (600000, 262144, 1),
+                                               (2200000, 40000, 1)])
 def test_embed_backward_exact_and_repeatable(S, tokens, vocab, cols):
     g = torch.Generator(DEV).manual_seed(tokens)
     ids = (vocab * torch.rand(tokens, device=DEV, generator=g) ** 4).long()
