@@ -615,8 +615,8 @@ size_t scape_token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int32_t
  * null if neither logp nor dlogp is asked for; top 0 goes with null lists.
  * With dlogits at least one of dlogp and dentropy is needed (null: zeros);
  * without it both have to be null.  dlogits may be logits' own matrix (same
- * data and ld).  1 <= vocab <= 2^20, 0 <= top <= min(vocab, 64), scale positive
- * and finite.
+ * data and ld).  1 <= vocab <= 2^20, 0 <= top <= min(vocab, 64), 2^-100 <=
+ * scale <= 2^100.
  *
  * Sums are fp32.  o is summed apart from the 1 it is added to, so logp and
  * entropy keep their relative precision where one word is all but certain.  A
@@ -637,7 +637,8 @@ scape_status scape_token_logprobs_backward(int64_t rows, int64_t vocab, scape_ma
 
 /* One gradient tensor of a list: count elements of type dtype at data, and
  * where its clipped values go: out of type out_dtype (dtype or fp32), which
- * may be data itself (then out_dtype = dtype).  out null: data itself. */
+ * may be data itself (then out_dtype = dtype).  out null: data itself.  Places
+ * that are written overlap no other tensor of the list. */
 typedef struct {
   const void* data;
   void* out;
@@ -654,7 +655,7 @@ size_t scape_grad_workspace_bytes(int32_t count, const scape_grad* grads, int32_
  * Norm of gradients over many tensors: the list is cut into `groups` equal
  * consecutive parts (count % groups == 0; one a worker, say), and
  *   norm[g] = scale * sqrt(sum over the tensors of part g of their squares)
- * scale (positive, finite) undoes a loss scale or a number of micro-batches.
+ * scale (2^-100 to 2^100) undoes a loss scale or a number of micro-batches.
  * Squares and sums are binary64, so no square overflows or is lost.
  */
 scape_status scape_grad_norm(int32_t count, const scape_grad* grads, int32_t groups, float scale, float* norm,

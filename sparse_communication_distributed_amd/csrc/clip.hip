@@ -12,6 +12,7 @@ namespace scape {
 namespace {
 
 constexpr int kSpans = 128;         // tensors of one launch: arguments of less than 4 KB
+constexpr int kFewSpans = 8;        // of a short list's: a call for one small tensor 9 us, with 4 KB to pass 13
 constexpr int kLaunchGroups = 4096;  // groups of one launch: 12 bits
 constexpr int64_t kPieces = 16384;  // pieces of a long list, about
 constexpr int kFewPieces = 1024;   // of a group: the clipping adds their sums itself
@@ -22,9 +23,10 @@ struct Span {
   uint64_t what;  // elements; from bit 48 on data's type, out's type, and the group less the launch's first
 };
 
+template <int NS>
 struct SpanArgs {
-  Span span[kSpans];
-  int32_t first[kSpans];  // piece of the whole list at which each span begins; past the last: none
+  Span span[NS];
+  int32_t first[NS];  // piece of the whole list at which each span begins; past the last: none
   int32_t begin;          // the first span's
   int32_t end;            // one past the last span's last piece
   int32_t group;          // of the first span
@@ -77,9 +79,13 @@ __device__ __forceinline__ double factor_of(double norm, const Scaling& s) {
 
 // The span of a piece: the number of those that begin at or before it, less
 // one, counted by all lanes at once.
-__device__ __forceinline__ int span_of(const SpanArgs& a, int32_t piece) {
+template <int NS>
+__device__ __forceinline__ int span_of(const SpanArgs<NS>& a, int32_t piece) {
   const int lane = threadIdx.x & 63;
-  return __popcll(__ballot(a.first[lane] <= piece)) + __popcll(__ballot(a.first[64 + lane] <= piece)) - 1;
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < NS; k += 64) n += __popcll(__ballot(k + lane < NS && a.first[k + lane] <= piece));
+  return n - 1;
 }
 
 struct Piece {
@@ -87,7 +93,8 @@ struct Piece {
   void* out;
   int64_t lo, hi;
   int dtype, out_dtype, group;
-  __device__ __forceinline__ Piece(const SpanArgs& a, int32_t piece) {
+  template <int NS>
+  __device__ __forceinline__ Piece(const SpanArgs<NS>& a, int32_t piece) {
     const int span = span_of(a, piece);
     const Span& s = a.span[span];
     data = s.data;
@@ -167,7 +174,8 @@ __device__ __forceinline__ double squares(const Piece& p) {
   return (sum[0] + sum[1]) + (sum[2] + sum[3]);
 }
 
-__global__ void __launch_bounds__(kThreads) grad_sum_kernel(SpanArgs a) {
+template <int NS>
+__global__ void __launch_bounds__(kThreads) grad_sum_kernel(SpanArgs<NS> a) {
   __shared__ double lds[kThreads / 64];
   const int32_t piece = a.begin + (int32_t)blockIdx.x;
   const Piece p(a, piece);
@@ -221,7 +229,8 @@ __device__ __forceinline__ void scale_some(const Piece& p, double f, bool stream
   else scale_piece<DT, OT, false>(p, f);
 }
 
-__global__ void __launch_bounds__(kThreads) grad_scale_kernel(SpanArgs a, Scaling s) {
+template <int NS>
+__global__ void __launch_bounds__(kThreads) grad_scale_kernel(SpanArgs<NS> a, Scaling s) {
   __shared__ double lds[kThreads / 64];
   const int32_t piece = a.end - 1 - (int32_t)blockIdx.x;
   const Piece p(a, piece);
@@ -260,6 +269,39 @@ int64_t pieces_of(int32_t count, const scape_grad* grads) {
   return n;
 }
 
+// The list's tensors in launches of at most NS: the sums of their pieces, or
+// (with `how`) their scaling.  per: tensors of a group.
+template <int NS>
+void launch_spans(int32_t count, const scape_grad* grads, int32_t per, int64_t piece, double* sums, const Scaling* how,
+                  hipStream_t s) {
+  SpanArgs<NS> a;
+  a.piece = piece;
+  a.sums = sums;
+  int32_t at = 0, n = 0;
+  for (int32_t i = 0; i <= count; ++i) {
+    const bool far = n > 0 && i < count && i / per - a.group >= kLaunchGroups;
+    if (n > 0 && (i == count || n == NS || far)) {
+      a.begin = a.first[0];
+      a.end = at;
+      for (int32_t j = n; j < NS; ++j) a.first[j] = INT32_MAX;
+      const dim3 grid((unsigned)(a.end - a.begin));
+      if (how) grad_scale_kernel<NS><<<grid, kThreads, 0, s>>>(a, *how);
+      else grad_sum_kernel<NS><<<grid, kThreads, 0, s>>>(a);
+      n = 0;
+    }
+    if (i == count || grads[i].count == 0) continue;
+    const scape_grad& g = grads[i];
+    if (n == 0) a.group = i / per;
+    a.first[n] = at;
+    Span& p = a.span[n++];
+    p.data = g.data;
+    p.out = g.out ? g.out : const_cast<void*>(g.data);
+    p.what = (uint64_t)g.count | (uint64_t)g.dtype << 48 | (uint64_t)(g.out ? g.out_dtype : g.dtype) << 50 |
+             (uint64_t)(i / per - a.group) << 52;
+    at += (int32_t)pieces(g.count, piece);
+  }
+}
+
 }  // namespace
 
 size_t grad_workspace(int32_t count, const scape_grad* grads, int32_t groups) {
@@ -290,34 +332,9 @@ hipError_t launch_grads(int32_t count, const scape_grad* grads, int32_t groups, 
   const Scaling how{alike ? nullptr : factors, norm, scale, max_norm, (int32_t)each, bytes > kStreamBytes};
 
   const auto walk = [&](bool scaling) {
-    SpanArgs a;
-    a.piece = piece;
-    a.sums = sums;
-    int32_t at = 0, n = 0;
-    for (int32_t i = 0; i <= count; ++i) {
-      const bool far = n > 0 && i < count && i / per - a.group >= kLaunchGroups;
-      if (n > 0 && (i == count || n == kSpans || far)) {
-        a.begin = a.first[0];
-        a.end = at;
-        for (int32_t j = n; j < kSpans; ++j) a.first[j] = INT32_MAX;
-        const dim3 grid((unsigned)(a.end - a.begin));
-        if (scaling) grad_scale_kernel<<<grid, kThreads, 0, s>>>(a, how);
-        else grad_sum_kernel<<<grid, kThreads, 0, s>>>(a);
-        n = 0;
-      }
-      if (i == count || grads[i].count == 0) continue;
-      const scape_grad& g = grads[i];
-      if (n == 0) a.group = i / per;
-      a.first[n] = at;
-      Span& p = a.span[n++];
-      p.data = g.data;
-      p.out = g.out ? g.out : const_cast<void*>(g.data);
-      p.what = (uint64_t)g.count | (uint64_t)g.dtype << 48 | (uint64_t)(g.out ? g.out_dtype : g.dtype) << 50 |
-               (uint64_t)(i / per - a.group) << 52;
-      at += (int32_t)pieces(g.count, piece);
-    }
+    if (count <= kFewSpans) launch_spans<kFewSpans>(count, grads, per, piece, sums, scaling ? &how : nullptr, s);
+    else launch_spans<kSpans>(count, grads, per, piece, sums, scaling ? &how : nullptr, s);
   };
-
   walk(false);
   if (!alike) {
     GroupArgs b;

@@ -35,7 +35,9 @@ scape_status check_logits(int64_t rows, int64_t vocab, int32_t top) {
 }
 
 scape_status check_scale(float scale) {
-  if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(SCAPE_EINVAL, "scale must be positive and finite");
+  // within 2^+-100, where its products with 32-bit constants keep their digits
+  if (!(scale >= 0x1p-100f) || !(scale <= 0x1p100f))
+    return fail(SCAPE_EINVAL, "scale must be positive and within 2^-100 and 2^100");
   return SCAPE_OK;
 }
 

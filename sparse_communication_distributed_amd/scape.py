@@ -881,9 +881,10 @@ class GradList:
     clipped values, tensors of as many elements and of the gradients' type or
     fp32, for instance parts of the optimizer's gradient rows; None: in place.
     It holds the tensors, not their values: a program that gets new gradient
-    tensors makes a new list."""
+    tensors makes a new list.  What clip_grads writes may overlap no other
+    tensor of the list."""
 
-    __slots__ = ("grads", "out", "groups", "device", "items")
+    __slots__ = ("grads", "out", "groups", "device", "items", "overlap")
 
     def __init__(self, grads, out=None, groups: int = 1):
         self.grads, self.groups = list(grads), int(groups)
@@ -909,6 +910,31 @@ class GradList:
                 raise ValueError(f"out[{i}] must have {g.numel()} elements (got {o.numel()})")
             if item.out_dtype not in (dt, 0):
                 raise ValueError(f"out[{i}] must be {g.dtype} or float32 (got {o.dtype})")
+        self.overlap = self._overlap()
+
+    def _overlap(self):
+        """The first tensor found that shares memory with a place that is
+        written for another one (or with a part of its own), or None."""
+        spans = []  # (begin, end, index, written)
+        for i, (g, item) in enumerate(zip(self.grads, self.items)):
+            if not item.count:
+                continue
+            size = item.count * g.element_size()
+            in_place = item.out is None or (item.out == item.data and item.out_dtype == item.dtype)
+            spans.append((item.data, item.data + size, i, in_place))
+            if not in_place:
+                spans.append((item.out, item.out + item.count * self.out[i].element_size(), i, True))
+        spans.sort()
+        read = written = None  # the spans of each kind that reach furthest
+        for s in spans:
+            for other in (read, written):
+                if other is not None and s[0] < other[1] and (s[3] or other[3]):
+                    return s[2]
+            if s[3]:
+                written = s if written is None or s[1] > written[1] else written
+            else:
+                read = s if read is None or s[1] > read[1] else read
+        return None
 
     def _check(self, t, name: str) -> int:
         try:
@@ -950,6 +976,8 @@ def clip_grads(grads: GradList, max_norm: float, norm, workspace, scale: float =
     to its place in out (or its own), and the norms to norm [groups].  A part
     whose norm is not finite is scaled and not clipped."""
     g = _grad_list(grads)
+    if g.overlap is not None:
+        raise ValueError(f"grads[{g.overlap}]: a place that is written overlaps another tensor of the list")
     ws, have = _workspace(workspace, grad_workspace_bytes(g), g.device)
     _enqueue(g.device, stream, lib().scape_grad_clip, len(g.grads), g.items, g.groups, scale, max_norm,
              _vector(norm, "norm", g.groups, g.device), ws, have)
