@@ -4,10 +4,9 @@
 // With m the largest logit, t = scale (x - m) and o the sum of e^t over all
 // words but one of the likeliest: logp = t_y - log(1 + o), entropy = log(1 + o)
 // - sum(e^t t) / (1 + o), and the gradient is a function of each logit alone.
-// Where the gradient is asked for, a row is read once, into registers, from
-// which the maximum, the sums and the gradient are taken; rows too long for
-// that are read again.  Without it a row passes by once, its sums kept relative
-// to the maximum so far.
+// A row is read once, into registers, from which the maximum, the sums and the
+// gradient are taken.  One too long for that passes by, its sums kept relative
+// to the maximum so far, and is read again for its gradient.
 #include "ends.h"
 
 #include <type_traits>
@@ -544,7 +543,10 @@ __device__ __forceinline__ int64_t load_target(const LogprobArgs& a, int64_t r, 
   return y;
 }
 
-// With the row in registers.  (Alternatives take the registers of a second
+// With the row in registers.  Bound by memory: 8192 x 32000 bf16 with the
+// gradient 195 us (1.05 GB, 5.4 TB/s), 4096 x 32000 bf16 without 57 us.  One row
+// of 32000 takes 5 us: half of that is arithmetic on one CU.
+// (Alternatives take the registers of a second
 // workgroup of a CU: forced into half, 2097 x 32001 bf16 with 20 of them takes 69
 // us instead of 83, but one row 11.2 instead of 9.6.)
 template <int DT, int T, int C, bool ENT, bool TOP>
@@ -687,7 +689,8 @@ __global__ void __launch_bounds__(T) logprobs_online_kernel(LogprobArgs a, int64
   if (a.dlogits.data) put_gradient<DT, T, ENT, true>(a, r, row, x, l);
 }
 
-// The gradient alone: T threads take kBackChunks chunks each of one row.
+// The gradient alone: T threads take kBackChunks chunks each of one row.  Bound by
+// memory: 1999 x 32000 fp32 75 us (512 MB, a part of them in the caches).
 constexpr int kBackChunks = 4;
 template <int DT, int T, bool STREAM>
 __global__ void __launch_bounds__(kThreads) logprobs_back_kernel(LogprobArgs a, int64_t pieces) {
