@@ -648,7 +648,8 @@ typedef struct {
 } scape_grad;
 
 /* Bytes of scratch of the two calls below for this list (256-byte aligned).
- * 0 if it is invalid.  The list itself is HOST memory, read during the call. */
+ * 0 if it is invalid.  count and groups are at most 2^20.  The list itself is
+ * HOST memory, read during the call. */
 size_t scape_grad_workspace_bytes(int32_t count, const scape_grad* grads, int32_t groups);
 
 /*

@@ -16,6 +16,7 @@ hipError_t launch_embed_backward(int64_t tokens, int64_t vocab, int64_t cols, co
                                  hipStream_t s);
 
 constexpr int kMaxTop = 64;
+constexpr int32_t kMaxGrads = 1 << 20;  // tensors of a list, and groups: a launch has a workgroup for each
 struct LogprobArgs {
   int64_t rows, vocab;
   scape_matrix logits;

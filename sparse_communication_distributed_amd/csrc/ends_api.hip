@@ -56,9 +56,9 @@ scape_status check_dlogits(const LogprobArgs& a) {
 }
 
 scape_status check_grads(int32_t count, const scape_grad* grads, int32_t groups, bool clip) {
-  if (count < 0 || groups < 1 || count % groups)
-    return fail(SCAPE_ESHAPE, "invalid list: count=%d groups=%d (need 0<=count, 1<=groups, count%%groups==0)", count,
-                groups);
+  if (count < 0 || count > kMaxGrads || groups < 1 || groups > kMaxGrads || count % groups)
+    return fail(SCAPE_ESHAPE, "invalid list: count=%d groups=%d (need 0<=count<=2^20, 1<=groups<=2^20, "
+                "count%%groups==0)", count, groups);
   if (count > 0 && !grads) return fail(SCAPE_EINVAL, "grads is null");
   int64_t total = 0;
   for (int32_t i = 0; i < count; ++i) {

@@ -129,6 +129,15 @@ def test_grad_list_refuses(items, groups, status):
     assert L.scape_grad_clip(len(g), g, groups, 1.0, 1.0, FAKE, FAKE, 1 << 40, None) == status
 
 
+@pytest.mark.parametrize("count,groups", [((1 << 20) + 1, 1), ((1 << 21), 1 << 21), (0, (1 << 20) + 1)])
+def test_grad_list_refuses_more_than_a_launch_holds(count, groups):
+    L = S.lib()
+    g = (S.Grad * max(count, 1))()  # counts of 0: refused by the list's length alone
+    assert L.scape_grad_workspace_bytes(count, g, groups) == 0
+    assert L.scape_grad_norm(count, g, groups, 1.0, FAKE, FAKE, 1 << 40, None) == SHAPE
+    assert L.scape_grad_clip(count, g, groups, 1.0, 1.0, FAKE, FAKE, 1 << 40, None) == SHAPE
+
+
 @pytest.mark.parametrize("item", [
     grad(out=2 * FAKE, out_dtype=FP16), grad(out=2 * FAKE, out_dtype=7), grad(out=2 * FAKE + 2, out_dtype=0),
     grad(out=FAKE, out_dtype=0),  # fp32 in the place of bf16
