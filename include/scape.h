@@ -547,7 +547,9 @@ scape_status scape_wgrad(int64_t rows, int64_t in, int64_t out, scape_matrix dy,
  * backward pass and the step.  Matrices, limits and the rules on overlapping
  * and on gradient rows are those of the activation operators; sizes called
  * vocab or positions count rows of a table or columns of logits.  Results are
- * deterministic: no sum depends on the order in which workgroups run.
+ * deterministic: no sum depends on the order in which workgroups run.  A row of
+ * logits is summed in an order that depends on where it begins between two
+ * 16-byte borders: copies that begin otherwise may differ by roundings.
  */
 
 /* Token numbers: a contiguous device array of 32- or 64-bit signed integers,

@@ -451,12 +451,25 @@ def test_token_logprobs_far_rows_and_empty(S):
     x.copy_(small)
     y, w = torch.arange(9, device=DEV), torch.randn(9, device=DEV)
     ws = scratch(S.token_logprobs_workspace_bytes(9, 70, 4))
+    # A row's sums are grouped by where its 16-byte borders lie, so bits are alike where rows begin alike: every
+    # 77 logits as every ld (both 5 past a multiple of 8).  Beside `small`, whose rows begin otherwise, a sum may
+    # have rounded in another order; each form is within the bound counted for a sum in any order.
+    assert ld % 8 == 77 % 8 and x.data_ptr() % 16 == 0
+    alike = torch.empty(9 * 77, dtype=torch.bfloat16, device=DEV).view(9, 77)[:, :70]
+    alike.copy_(small)
+    assert alike.data_ptr() % 16 == 0
+    b = Bounds(f64(small), 1.0)
+    want, tol = b.gradient(f64(small), np.arange(9), f64(w), None, 1.0, torch.bfloat16)
     res = []
-    for m in (x, small):
+    for m in (x, alike, small):
+        logits = f64(m)
         logp, ids = torch.empty(9, device=DEV), torch.empty(9, 4, dtype=torch.int32, device=DEV)
         S.token_logprobs(m, y, logp, ws, top_ids=ids, dlogp=w, dlogits=m)
         res.append((logp, ids, m.clone()))
-    assert all(torch.equal(a, b) for a, b in zip(*res))
+        within(logp, E.token_logp(logits, np.arange(9), 1.0), b.dlp[np.arange(9), np.arange(9)], "logp")
+        within(m, want, tol, "dlogits")
+    assert all(torch.equal(a, b) for a, b in zip(*res[:2]))
+    assert torch.equal(res[0][1], res[2][1])
     none = torch.empty(0, 70, device=DEV)
     S.token_logprobs(none, y[:0], logp[:0], scratch(S.token_logprobs_workspace_bytes(0, 70, 0)))
     S.token_logprobs_backward(none, y[:0], torch.empty(0, 2, device=DEV), none, dlogp=w[:0])
