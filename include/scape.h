@@ -667,7 +667,8 @@ scape_status scape_grad_norm(int32_t count, const scape_grad* grads, int32_t gro
 /*
  * Clipping by that norm:
  *   out = data * (scale * min(1, max_norm / norm[g]))
- * rounded once; norm [groups] is written as above.  A part whose norm is not
+ * the product formed in binary64 and rounded from there to out's type; norm
+ * [groups] is written as above.  A part whose norm is not
  * finite is scaled and not clipped.  In place, a part with the factor 1 is not
  * written.  max_norm is positive (infinite: scale only).
  */

@@ -227,6 +227,20 @@ __global__ void __launch_bounds__(kNormThreads) grad_norm_kernel(GroupArgs a) {
   if (a.clip) a.factors[g] = factor_of(norm, a.s);
 }
 
+// A binary64 product as fp32 that Elem<OT>::put rounds as it would the product
+// itself.  For 16 bits fp32 takes the neighbour towards zero with its last bit
+// set wherever digits are lost: that is neither a 16-bit value nor halfway
+// between two of them, so what is next to one of these stays on its side.
+template <int OT>
+__device__ __forceinline__ float narrowed(double x) {
+  const float f = (float)x;
+  if (OT == SCAPE_F32) return f;
+  const double back = f;
+  uint32_t u = __float_as_uint(f);
+  if (back != x) u = (u - (fabs(back) > fabs(x) ? 1u : 0u)) | 1u;
+  return __uint_as_float(u);
+}
+
 template <int DT, int OT, bool STREAM>
 __device__ __forceinline__ void scale_piece(const Piece& p, double f) {
   // 16 bytes of the wider side a lane, so that neighbouring lanes' accesses
@@ -238,17 +252,17 @@ __device__ __forceinline__ void scale_piece(const Piece& p, double f) {
       [&](int64_t i, const Some<DT, N>& x) {
         float v[N];
         x.widen(v);
-        // one rounding: the product is exact in 64 bits, or next to it
+        // one rounding of the binary64 product, which is exact or next to it
         typename Elem<OT>::T o[N];
 #pragma unroll
-        for (int j = 0; j < N; ++j) Elem<OT>::put(o, j, (float)((double)v[j] * f));
+        for (int j = 0; j < N; ++j) Elem<OT>::put(o, j, narrowed<OT>((double)v[j] * f));
         u32x4 w;
         __builtin_memcpy(&w, o, 16);
         u32x4_any* q = reinterpret_cast<u32x4_any*>(static_cast<typename Elem<OT>::T*>(p.out) + i);
         if (STREAM) __builtin_nontemporal_store(w, q);
         else *q = w;
       },
-      [&](int64_t i) { Elem<OT>::put(p.out, i, (float)((double)Elem<DT>::get(p.data, i) * f)); });
+      [&](int64_t i) { Elem<OT>::put(p.out, i, narrowed<OT>((double)Elem<DT>::get(p.data, i) * f)); });
 }
 
 template <int DT, int OT>
