@@ -439,24 +439,45 @@ __device__ __forceinline__ int64_t partial_rows(const ChunkArgs& a, int32_t k, u
   *word = w;
   if (w == kNoWord || after != w) return 0;
   if (first == w && p0 > 0 && before == w) return 0;  // begins further ahead
-  int64_t n = 1;
-  for (int64_t at = k + 1;;) {
-    const uint64_t others = __ballot(begins != w);
-    n += others ? __builtin_ctzll(others) : 64;
-    if (others) return n;
-    at += 64;
-    begins = begin_of(at + (threadIdx.x & 63));
+  const uint64_t others = __ballot(begins != w);
+  if (others) return 1 + __builtin_ctzll(others);
+  // the first chunk behind these that begins with another word: 64 of what is
+  // left are looked at a time, since the words are sorted
+  int64_t lo = k + 65, hi = a.chunks;
+  while (lo < hi) {
+    const int64_t step = (hi - lo + 63) / 64;
+    const int64_t at = lo + (threadIdx.x & 63) * step;
+    const uint64_t past = __ballot(at >= hi || begin_of(at) != w);
+    const int first_past = past ? __builtin_ctzll(past) : 64;
+    if (first_past == 0) break;
+    const int64_t end = lo + first_past * step;
+    hi = end < hi ? end : hi;
+    lo += (first_past - 1) * step + 1;
   }
+  return lo - k;
 }
 
-// The sum of partial rows [from, to) of chunk k's word at columns [c, c + 4).
+// The sum of partial rows [from, to) of chunk k's word at columns [c, c + 4),
+// eight at a time in pairs: they are on the way together, and a long sum is an
+// eighth as many additions deep.
 __device__ __forceinline__ f32x4 part_sum(const ChunkArgs& a, int32_t k, int64_t from, int64_t to, int64_t c) {
+  constexpr int kAtOnce = 8;
+  const auto row = [&](int64_t i) {
+    return *reinterpret_cast<const f32x4*>(a.part + ((k + i) * 2 + (i == 0 ? 1 : 0)) * a.pitch + c);
+  };
   f32x4 sum = {0, 0, 0, 0};
-#pragma unroll 8
-  for (int64_t i = from; i < to; ++i) {
-    const float* p = a.part + ((k + i) * 2 + (i == 0 ? 1 : 0)) * a.pitch + c;
-    sum += *reinterpret_cast<const f32x4*>(p);
+  int64_t i = from;
+  for (; i + kAtOnce <= to; i += kAtOnce) {
+    f32x4 x[kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) x[j] = row(i + j);
+#pragma unroll
+    for (int d = 1; d < kAtOnce; d *= 2)
+#pragma unroll
+      for (int j = 0; j < kAtOnce; j += 2 * d) x[j] += x[j + d];
+    sum += x[0];
   }
+  for (; i < to; ++i) sum += row(i);
   return sum;
 }
 
@@ -468,35 +489,51 @@ __device__ __forceinline__ void put_sum(const ChunkArgs& a, uint32_t w, int64_t 
 }
 
 // Joins the sums of words that cross chunks: a wave a chunk, 4 columns a lane.
-// Where a word has many partial rows the four waves add a quarter of them each,
-// in order, then the quarters.  6 us for 511 borders of 2048 columns, the latency
-// of three loads.
+// A word with many partial rows (only one can begin in the chunks of a
+// workgroup) is shared by all waves, and by the groups of lanes of a wave where
+// a row has fewer than 256 columns, a consecutive part each, joined in a fixed
+// order.  Ordinary words: 6 us for 511 borders of 2048 columns, the latency of
+// three loads.  65536 tokens of one word, 64 and 1024 columns, all of the call:
+// 114 and 172 us; in four parts, read one after the other, 283 and 201.  (16
+// waves: 114 and 136, but 0.5 to 1 us more for ordinary words.)
 constexpr int kLongJoin = 16;
-__global__ void __launch_bounds__(kThreads) embed_join_kernel(ChunkArgs a) {
-  __shared__ f32x4 lds[3][64];
-  __shared__ int64_t rows[4];
-  __shared__ uint32_t words[4];
+constexpr int kJoinWaves = 8;
+__global__ void __launch_bounds__(kJoinWaves * 64) embed_join_kernel(ChunkArgs a) {
+  __shared__ f32x4 lds[kJoinWaves][64];
+  __shared__ int64_t rows[kJoinWaves];
+  __shared__ uint32_t words[kJoinWaves];
   const int q = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int64_t c = ((int64_t)blockIdx.y * 64 + lane) * 4;
-  const bool mine = c < a.pitch;
-  for (int64_t k0 = (int64_t)blockIdx.x * 4; k0 + 1 < a.chunks; k0 += (int64_t)gridDim.x * 4) {
+  const int64_t c0 = (int64_t)blockIdx.y * 256, c = c0 + lane * 4;
+  for (int64_t k0 = (int64_t)blockIdx.x * kJoinWaves; k0 + 1 < a.chunks; k0 += (int64_t)gridDim.x * kJoinWaves) {
     const int32_t k = (int32_t)k0 + q;
     uint32_t w = kNoWord;
     const int64_t n = k + 1 < a.chunks ? partial_rows(a, k, &w) : 0;
-    if (n > 0 && n <= kLongJoin && mine) put_sum(a, w, c, part_sum(a, k, 0, n, c));
+    if (n > 0 && n <= kLongJoin && c < a.pitch) put_sum(a, w, c, part_sum(a, k, 0, n, c));
     if (lane == 0) {
       rows[q] = n > kLongJoin ? n : 0;
       words[q] = w;
     }
     __syncthreads();
-    for (int b = 0; b < 4; ++b) {
+    const uint64_t is_long = __ballot(rows[lane % kJoinWaves] != 0);
+    if (is_long) {
+      const int b = __builtin_ctzll(is_long);
       const int64_t m = rows[b];
-      if (m == 0) continue;
-      const f32x4 sum = mine ? part_sum(a, (int32_t)k0 + b, m * q / 4, m * (q + 1) / 4, c) : f32x4{0, 0, 0, 0};
-      if (q > 0) lds[q - 1][lane] = sum;
+      int across = 64;  // lanes that share a row, a power of two
+      while (across > 1 && c0 + across * 2 >= a.pitch) across /= 2;
+      const int parts = kJoinWaves * (64 / across), part = q * (64 / across) + lane / across;
+      const int64_t mine = c0 + (lane & (across - 1)) * 4;
+      f32x4 sum = {0, 0, 0, 0};
+      if (mine < a.pitch) sum = part_sum(a, (int32_t)k0 + b, m * part / parts, m * (part + 1) / parts, mine);
+      for (int d = across; d < 64; d *= 2)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[j] += __shfl_xor(sum[j], d, 64);
+      lds[q][lane] = sum;
       __syncthreads();
-      if (q == 0 && mine) put_sum(a, words[b], c, ((sum + lds[0][lane]) + lds[1][lane]) + lds[2][lane]);
-      __syncthreads();
+      if (q == 0 && lane < across && mine < a.pitch) {
+#pragma unroll
+        for (int i = 1; i < kJoinWaves; ++i) sum += lds[i][lane];
+        put_sum(a, words[b], mine, sum);
+      }
     }
     __syncthreads();  // rows and words have been read
   }
@@ -569,7 +606,11 @@ void embed_out(const EmbedArgs& a, int out, hipStream_t s) {
 // Words that a workgroup of the slab sort owns: about one workgroup a CU.  0:
 // sorted by tiles, which can be any number.  16384 tokens of 32000 words: slabs
 // 7.5 us, tiles and their merge 16.5; 1531 of 4099: 5.2 against 10.5; 65536 of
-// 32000 x 1024, all of the call: 184 against 222.
+// 32000 x 1024, all of the call: 184 against 222.  Few words share few
+// workgroups, and still: 8 columns, all of the call, 262144 tokens of 2 words 286
+// against 320, of 1024 104 against 307, 1048576 of 2 1150 against 1870.  (Tiles
+// win where a word of many has most tokens, which is not known here: 262144 of
+// 32000 x 64, half of them one word, 408 against 310.)
 int slab_of(int64_t tokens, int64_t vocab) {
   int slab = 4;
   while (slab < kSlabMax && (vocab + slab - 1) / slab > 256) slab *= 2;
@@ -647,8 +688,8 @@ hipError_t launch_embed_backward(int64_t tokens, int64_t vocab, int64_t cols, co
   else if (dy.dtype == SCAPE_BF16) launch_chunks<SCAPE_BF16>(ca, grid, s);
   else launch_chunks<SCAPE_F16>(ca, grid, s);
   if (p.chunks > 1)
-    embed_join_kernel<<<dim3(capped((p.chunks + 2) / 4, 1 << 20), (unsigned)((p.pitch + 255) / 256)), kThreads, 0, s>>>(
-        ca);
+    embed_join_kernel<<<dim3(capped((p.chunks + kJoinWaves - 2) / kJoinWaves, 1 << 20), (unsigned)((p.pitch + 255) / 256)),
+                        kJoinWaves * 64, 0, s>>>(ca);
   return hipGetLastError();
 }
 

@@ -65,3 +65,52 @@ def test_clipped_values_are_rounded_once(S, t):
             got = (src if out is None else out).double().cpu().numpy()
             assert np.array_equal(got, want), (f, np.flatnonzero(got != want)[:5])
     assert missed > 100  # factors at which a second rounding shows
+
+
+# ----------------------------------------------------------------- embedding
+
+U = 2.0 ** -24
+
+
+@pytest.mark.parametrize("tokens,cols,depth", [(1 << 20, 8, 64), (1 << 18, 8, 64), (200001, 320, 150)])
+def test_embed_backward_frequent_word_keeps_its_digits(S, tokens, cols, depth):
+    """All tokens one word, all rows one number: roundings that all go one way,
+    so the error grows with the number of additions behind one another.  Those of
+    a chunk of 32, of an eighth of a part's partial rows, in pairs and of the
+    parts are `depth` at most."""
+    for value in (1.1, 0.3, 1.7):
+        dy = torch.full((tokens, cols), value, device=DEV)
+        value = float(np.float32(value))
+        out = torch.empty(2, cols, device=DEV)
+        ws = scratch(S.embed_workspace_bytes(tokens, cols))
+        S.embed_backward(torch.zeros(tokens, dtype=torch.int64, device=DEV), dy, out, ws)
+        want = tokens * value
+        off = (out[0].double().cpu().numpy() / want - 1) / U
+        assert np.abs(off).max() <= depth, off
+        assert (out[1] == 0).all()
+
+
+@pytest.mark.parametrize("tokens,cols", [(70000, 4), (70000, 20), (40000, 130), (30000, 300), (600000, 9), (9000, 1030)])
+def test_embed_backward_runs_of_every_length(S, tokens, cols):
+    """Words with 0 to thousands of partial rows in turn, at every place among the
+    chunks: whole numbers, whose sums are exact in any order."""
+    r = np.random.default_rng(cols)
+    sizes = [tokens // 3, 1, 511, 512, 513, 40, 8 * 64 + 7, 8 * 65, 16 * 64 - 1, 16 * 65 + 9, 32 * 17, 32 * 64 + 33,
+             32 * 66, 7, 2]
+    sizes = [s for s in sizes if s < tokens // 2]
+    while sum(sizes) < tokens:
+        sizes.append(int(min(tokens - sum(sizes), np.exp(r.uniform(0, np.log(4000))))))
+    cut = np.cumsum(sizes)
+    sizes = sizes[:int(np.searchsorted(cut, tokens, side="right"))]
+    word = np.repeat(np.arange(len(sizes)), sizes)
+    word = np.concatenate([word, np.full(tokens - word.size, len(sizes))])
+    ids = torch.from_numpy(r.permutation(word)).to(DEV)
+    vocab = len(sizes) + 3
+    dy = torch.from_numpy(r.integers(-8, 9, (tokens, cols))).to(DEV).to(torch.bfloat16)
+    want = torch.zeros(vocab, cols, dtype=torch.float64, device=DEV).index_add_(0, ids, dy.double())
+    out = torch.full((vocab, cols), 2.0, device=DEV)
+    ws = scratch(S.embed_workspace_bytes(tokens, cols))
+    S.embed_backward(ids, dy, out, ws, scale=0.5)
+    assert torch.equal(out.double(), 0.5 * want)
+    S.embed_backward(ids, dy, out, ws, accumulate=True, scale=0.5)
+    assert torch.equal(out.double(), want)
