@@ -582,8 +582,9 @@ size_t scape_embed_workspace_bytes(int64_t tokens, int64_t cols);
  * added to what dtable holds if accumulate is not 0 (rows of no token then
  * stay as they are; otherwise they are set to zero).  dtable is contiguous
  * fp32 [vocab][cols], and may be a tensor's part of a row of grads.  dy of no
- * token is not read.  Sums are fp32, of at most a few dozen rows each, which are
- * joined in the tokens' order.  A table of positions takes a call of its own, with
+ * token is not read.  Sums are fp32, of at most 32 rows each, which are joined in
+ * a fixed order: of a word's N rows no more than N / 512 + 64 are added one
+ * behind the other.  A table of positions takes a call of its own, with
  * pos in the place of ids.
  */
 scape_status scape_embed_backward(int64_t tokens, int64_t vocab, int64_t cols, scape_ids ids, scape_matrix dy,
