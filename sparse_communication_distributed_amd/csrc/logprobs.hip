@@ -461,14 +461,24 @@ struct RowGradient {
 template <int DT, bool ENT, bool STREAM, int M>
 __device__ __forceinline__ void emit_some(const RowGradient& g, char* out, int first, Number<M> n, int vocab, float* v) {
   if (first >= vocab) return;
-  if (g.none) {
-#pragma unroll
-    for (int j = 0; j < n; ++j) v[j] = 0.0f;
-  } else {
-    g.of<ENT>(v, n);
-  }
+  g.of<ENT>(v, n);
   if (n > 1) Chunk<DT>::template store<STREAM>(out, first, v);
   else Elem<DT>::put(out, first, v[0]);
+}
+
+// Zeros for the units [from, to) of a row, chunks and behind them single logits,
+// every T-th of them: what a row without a gradient gets, which is not read.
+template <int DT, int T, bool STREAM>
+__device__ __forceinline__ void put_zeros(const Cut<DT>& row, char* out, int from, int to) {
+  constexpr int N = Cut<DT>::N;
+  float zeros[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) zeros[j] = 0.0f;
+  const int units = row.whole + row.singles();
+  for (int i = from; i < to && i < units; i += T) {
+    if (i < row.whole) Chunk<DT>::template store<STREAM>(out, row.chunk(i), zeros);
+    else Elem<DT>::put(out, row.single(i - row.whole), 0.0f);
+  }
 }
 
 // ------------------------------------------------------------------- kernels
@@ -517,11 +527,15 @@ __device__ __forceinline__ void put_gradient(const LogprobArgs& a, int64_t r, R&
                                              const RowLds<T>& l) {
   const RowGradient g(a, r, x.m, x.ls, x.h);
   char* const out = static_cast<char*>(a.dlogits.data) + r * a.dlogits.ld * Chunk<DT>::kSize;
+  if (g.none) {
+    put_zeros<DT, T, STREAM>(row, out, Team<T>::thread(), INT32_MAX);
+    return;
+  }
   row.each([&](int first, auto n, float* v) {
     emit_some<DT, ENT, STREAM>(g, out, first, n, n > 1 ? row.chunks_end() : row.vocab, v);
   });
   // by the thread that wrote its place before
-  if (g.none || g.y < 0) return;
+  if (g.y < 0) return;
   const int unit = row.unit_of(g.y);
   if (Team<T>::thread() == (unit < row.whole ? unit % T : unit - row.whole))
     Elem<DT>::put(out, g.y, g.at_target(l.target));
@@ -706,9 +720,13 @@ __global__ void __launch_bounds__(kThreads) logprobs_back_kernel(LogprobArgs a, 
     char* const out = static_cast<char*>(a.dlogits.data) + r * a.dlogits.ld * Chunk<DT>::kSize;
     constexpr int N = Chunk<DT>::N;
     const Cut<DT> row(in, a.vocab);
+    if (g.none) {  // of all threads that share the row
+      put_zeros<DT, T, STREAM>(row, out, i0, i0 + kBackChunks * T);
+      continue;
+    }
     // in logits' place the target's is read before its chunk is written, by the same thread
     const int unit = row.unit_of(g.y);
-    const bool mine = !g.none && g.y >= 0 && unit >= i0 && (unit - i0) % T == 0 && unit - i0 < kBackChunks * T;
+    const bool mine = g.y >= 0 && unit >= i0 && (unit - i0) % T == 0 && unit - i0 < kBackChunks * T;
     const float target = mine ? Elem<DT>::get(in, g.y) : 0.0f;
     const auto emit = [&](auto with_entropy) {
       constexpr bool ent = decltype(with_entropy)::value;

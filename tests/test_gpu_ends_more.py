@@ -114,3 +114,53 @@ def test_embed_backward_runs_of_every_length(S, tokens, cols):
     assert torch.equal(out.double(), 0.5 * want)
     S.embed_backward(ids, dy, out, ws, accumulate=True, scale=0.5)
     assert torch.equal(out.double(), want)
+
+
+# --------------------------------------------------------- log probabilities
+
+
+@pytest.mark.parametrize("t", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("vocab", [1, 5, 900, 1031, 4099, 33001, 70001])
+def test_token_logprobs_rows_of_no_weight(S, vocab, t):
+    """A row without a weight gets zeros from either call, in place or not, into
+    rows that begin anywhere, whatever its logits and stats are; its neighbours
+    keep their gradients, and nothing beside the rows is written."""
+    rows, lead = 6, 3
+    x = torch.randn(rows, vocab, device=DEV)
+    y = torch.arange(rows, device=DEV) % vocab
+    w = torch.tensor([1.0, 0.0, -2.0, 0.0, 0.0, 0.5], device=DEV)
+    d = torch.tensor([0.0, 0.0, 1.0, 0.0, 0.0, 0.0], device=DEV)
+    y[3] = -100
+    w[3] = INF  # of no token: no weight
+    none = torch.tensor([1, 3, 4], device=DEV)
+    ws = scratch(S.token_logprobs_workspace_bytes(rows, vocab, 0))
+    x = x.to(t)
+    bare = x.clone()
+    bare[1], bare[3], bare[4] = float("nan"), INF, float("nan")
+    logp, h, stats = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV), torch.empty(rows, 2, device=DEV)
+    for ent in (None, d):
+        res = []
+        for logits in (x, bare):
+            for fused in (True, False):
+                for in_place in (False, True):
+                    ld = vocab + 5
+                    buf = torch.full((rows * ld + 16,), 7.0, dtype=t, device=DEV)
+                    out = buf[lead:lead + rows * ld].view(rows, ld)[:, :vocab]
+                    src = logits
+                    if in_place:
+                        out.copy_(logits)
+                        src = out
+                    kw = dict(dlogp=w, dentropy=ent)
+                    S.token_logprobs(src, y, logp, ws, stats=stats, entropy=h, **(dict(kw, dlogits=out) if fused else {}))
+                    if not fused:
+                        S.token_logprobs_backward(src, y, stats, out, entropy=h, **kw)
+                    assert (out[none] == 0).all(), (fused, in_place)
+                    res.append(out[[0, 2, 5]].double())
+                    inside = torch.zeros_like(buf, dtype=torch.bool)
+                    inside[lead:lead + rows * ld].view(rows, ld)[:, :vocab] = True
+                    assert (buf[~inside] == 7).all()
+        if vocab > 1:
+            assert all(torch.isfinite(r).all() and r.abs().sum() > 0 for r in res)
+        # the logits beside a row change nothing in it
+        for a, b in zip(res[:4], res[4:]):
+            assert torch.equal(a, b)
