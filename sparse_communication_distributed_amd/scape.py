@@ -880,11 +880,13 @@ class GradList:
     have a norm each, one a worker, say.  ``out``: where clip_grads puts the
     clipped values, tensors of as many elements and of the gradients' type or
     fp32, for instance parts of the optimizer's gradient rows; None: in place.
-    It holds the tensors, not their values: a program that gets new gradient
-    tensors makes a new list.  What clip_grads writes may overlap no other
-    tensor of the list."""
+    It is a list of memory, not of values: it keeps the memory that the tensors
+    had when it was made (whose storages may not be resized while it is in
+    use).  A program that gets new gradient tensors, or gives one of these
+    other memory by ``.data``, makes a new list.  What clip_grads writes may
+    overlap no other tensor of the list."""
 
-    __slots__ = ("grads", "out", "groups", "device", "items", "overlap")
+    __slots__ = ("grads", "out", "groups", "device", "items", "overlap", "storages")
 
     def __init__(self, grads, out=None, groups: int = 1):
         self.grads, self.groups = list(grads), int(groups)
@@ -911,6 +913,8 @@ class GradList:
             if item.out_dtype not in (dt, 0):
                 raise ValueError(f"out[{i}] must be {g.dtype} or float32 (got {o.dtype})")
         self.overlap = self._overlap()
+        # A tensor may be given other memory later: what is at its old address must stay memory of this list.
+        self.storages = [t.untyped_storage() for t in self.grads + (self.out or [])]
 
     def _overlap(self):
         """The first tensor found that shares memory with a place that is

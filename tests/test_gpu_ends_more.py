@@ -164,3 +164,30 @@ def test_token_logprobs_rows_of_no_weight(S, vocab, t):
         # the logits beside a row change nothing in it
         for a, b in zip(res[:4], res[4:]):
             assert torch.equal(a, b)
+
+
+# --------------------------------------------------------------------- lists
+
+
+def test_grad_list_whose_tensors_moved(S):
+    """Tensors given other memory: the list goes on with its own, and what the
+    program allocates since is left as it is."""
+    a, row = torch.full((100000,), 2.0, device=DEV), torch.zeros(100000, device=DEV)
+    norm = torch.full((1,), -1.0, device=DEV)
+    for gl in (S.GradList([a]), S.GradList([a], out=[row])):
+        ws = scratch(S.grad_workspace_bytes(gl))
+        kept = a.detach()
+        a.data = torch.full((100000,), 5.0, device=DEV)
+        if gl.out:
+            row.data = torch.zeros(100000, device=DEV)
+        del kept  # the list alone holds the old memory
+        new = [torch.full((100000,), 7.0, device=DEV) for _ in range(6)]
+        S.clip_grads(gl, INF, norm, ws, scale=0.25)
+        assert (a == 5).all() and (row == 0).all() and all((t == 7).all() for t in new)
+        S.grad_norm(gl, norm, ws)
+        if gl.out is None:
+            assert abs(norm.item() / (0.5 * 100000 ** 0.5) - 1) < 1e-6
+        a.data = torch.full((100000,), 2.0, device=DEV)
+    # a new list takes the new memory
+    S.clip_grads(S.GradList([a], out=[row]), INF, norm, ws, scale=2.0)
+    assert (row == 4).all() and (a == 2).all()
