@@ -113,12 +113,16 @@ __global__ void __launch_bounds__(kThreads) embed_sort_kernel(SortArgs a) {
 // words and goes through all tokens.  Its waves take a stretch of them each,
 // list those of the slab in LDS and count them by word; a token's place is the
 // number of tokens of lower words, of the same word in the stretches before,
-// and of the same word before it in its own.  Where the lists have no room for
-// all tokens, the waves go through their stretch a second time instead.
+// and of the same word before it in its own.  Where a list has no room for all
+// of a stretch, the waves go through it a second time instead.
 constexpr int kSlabThreads = 1024;
 constexpr int kSlabWaves = kSlabThreads / 64;
 constexpr int kSlabMax = 512;
-constexpr int64_t kListTokens = 16384;           // the lists' room
+// LDS for counts and lists: a CU's 160 KB, less 8 for what else the kernel holds.
+// 32000 words x 64, all of the call, with lists and with a second walk: 20000
+// tokens 24.3 and 32.7 us, 36000 tokens 29.4 and 45.1; 131072 words, 30000 tokens
+// 29.2 and 41.6.
+constexpr int64_t kSlabLds = 152 << 10;
 constexpr int64_t kSlabs = 1024;                 // workgroups at most: each goes through all tokens
 constexpr int64_t kSlabWork = int64_t(1) << 28;  // tokens that they go through in all, at most
 constexpr int kAhead = 8;                        // tokens of a lane on the way at a time
@@ -666,7 +670,8 @@ hipError_t launch_embed_backward(int64_t tokens, int64_t vocab, int64_t cols, co
     const int stretch = (int)((tokens + kSlabThreads - 1) / kSlabThreads) * 64;
     const SlabArgs a{tokens, vocab, p.padded, ids.data, slab, stretch, at(p.word[0]), at(p.token[0])};
     const dim3 grid((unsigned)((vocab + slab - 1) / slab));
-    const bool list = tokens <= kListTokens;
+    // (a stretch that passes is far below the 2^16 places of a list's entry)
+    const bool list = (int64_t)(slab + stretch) * kSlabWaves * 4 <= kSlabLds;
     const size_t lds = (size_t)(slab + (list ? stretch : 0)) * kSlabWaves * 4;
     const auto go = [&](auto kernel) { kernel<<<grid, kSlabThreads, lds, s>>>(a); };
     if (ids.bits == 64) go(list ? embed_slab_kernel<int64_t, true> : embed_slab_kernel<int64_t, false>);

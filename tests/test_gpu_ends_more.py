@@ -72,6 +72,12 @@ def test_clipped_values_are_rounded_once(S, t):
 U = 2.0 ** -24
 
 
+def table_of(ids, dy, vocab):
+    """The sums of whole numbers dy [tokens][cols] (host) by word, on the device; ids may hold -1."""
+    return torch.from_numpy(np.stack([np.bincount(ids + 1, weights=column, minlength=vocab + 1)[1:] for column in dy.T],
+                                     axis=1)).to(DEV)
+
+
 @pytest.mark.parametrize("tokens,cols,depth", [(1 << 20, 8, 64), (1 << 18, 8, 64), (200001, 320, 150)])
 def test_embed_backward_frequent_word_keeps_its_digits(S, tokens, cols, depth):
     """All tokens one word, all rows one number: roundings that all go one way,
@@ -104,16 +110,40 @@ def test_embed_backward_runs_of_every_length(S, tokens, cols):
     sizes = sizes[:int(np.searchsorted(cut, tokens, side="right"))]
     word = np.repeat(np.arange(len(sizes)), sizes)
     word = np.concatenate([word, np.full(tokens - word.size, len(sizes))])
-    ids = torch.from_numpy(r.permutation(word)).to(DEV)
+    word = r.permutation(word)
+    ids = torch.from_numpy(word).to(DEV)
     vocab = len(sizes) + 3
-    dy = torch.from_numpy(r.integers(-8, 9, (tokens, cols))).to(DEV).to(torch.bfloat16)
-    want = torch.zeros(vocab, cols, dtype=torch.float64, device=DEV).index_add_(0, ids, dy.double())
+    whole = r.integers(-8, 9, (tokens, cols))
+    dy = torch.from_numpy(whole).to(DEV).to(torch.bfloat16)
+    want = table_of(word, whole, vocab)
     out = torch.full((vocab, cols), 2.0, device=DEV)
     ws = scratch(S.embed_workspace_bytes(tokens, cols))
     S.embed_backward(ids, dy, out, ws, scale=0.5)
     assert torch.equal(out.double(), 0.5 * want)
     S.embed_backward(ids, dy, out, ws, accumulate=True, scale=0.5)
     assert torch.equal(out.double(), want)
+
+
+@pytest.mark.parametrize("tokens,vocab", [(37888, 1000), (37889, 1000), (36864, 32000), (36865, 32000), (30720, 131072),
+                                          (30721, 131072), (24001, 60000)])
+def test_embed_backward_where_the_sort_changes(S, tokens, vocab):
+    """As many tokens as the sort's lists hold and one more; every word's sum
+    exact, and all tokens one word, which fills the lists of one workgroup."""
+    r = np.random.default_rng(tokens)
+    whole = r.integers(-8, 9, (tokens, 9))
+    dy = torch.from_numpy(whole).to(DEV).to(torch.bfloat16)
+    out = torch.empty(vocab, 9, device=DEV)
+    ws = scratch(S.embed_workspace_bytes(tokens, 9))
+    some = (vocab * r.random(tokens) ** 2).astype(np.int64)
+    some[r.random(tokens) < 0.1] = -1
+    for ids in (some, np.full(tokens, vocab - 1), np.arange(tokens) % vocab):
+        t = torch.from_numpy(ids).to(DEV)
+        want = table_of(ids, whole, vocab)
+        S.embed_backward(t, dy, out, ws)
+        assert torch.equal(out.double(), want)
+        ws.fill_(0xA5)
+        S.embed_backward(t.int(), dy, out, ws)
+        assert torch.equal(out.double(), want)
 
 
 # --------------------------------------------------------- log probabilities
