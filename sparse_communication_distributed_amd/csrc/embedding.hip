@@ -544,11 +544,14 @@ __global__ void __launch_bounds__(kJoinWaves * 64) embed_join_kernel(ChunkArgs a
 }
 
 // Rows of no token are cleared past the caches where the table and dy together
-// are more than they hold.  Table of 32000 x 2048 (250 MiB), with the forward
-// pass, past the caches and through them: 16384 tokens 95 and 116 us, 4096
-// tokens 72 and 70, 64 tokens 60 and 49; 50257 x 1024 (196 MiB), 8192 tokens: the
-// launch that clears 42 and 32.
-constexpr int64_t kClearStream = int64_t(288) << 20;
+// are more than a part of them.  Inputs and tables that change from pass to pass,
+// with the forward pass, us past the caches and through them: table and dy of 62
+// and 8 MiB 31.9 and 31.0, 93 and 0.1 27.9 and 26.8, 93 and 8 37.7 and 39.9, 125
+// and 16 49.3 and 52.0, 196 and 16 (50257 x 1024, 8192 tokens) 63.3 and 68.1, 250
+// and 64 (32000 x 2048, 16384 tokens) 109 and 114.6.  (One table over and over,
+// with nothing beside it, stays in the caches: 250 MiB and 64 tokens 58 and 44.
+// A training step moves more than they hold between two of its gradients.)
+constexpr int64_t kClearStream = int64_t(96) << 20;
 
 // How a gradient's tokens are cut, and its workspace.
 struct BackPlan {

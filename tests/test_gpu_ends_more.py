@@ -146,6 +146,28 @@ def test_embed_backward_where_the_sort_changes(S, tokens, vocab):
         assert torch.equal(out.double(), want)
 
 
+@pytest.mark.parametrize("vocab,cols", [(24400, 1024), (24590, 1024), (24001, 1021), (25001, 1021), (2000000, 13)])
+def test_embed_backward_clears_large_tables(S, vocab, cols):
+    """Rows of no token are zero, at tables on both sides of the size from which
+    they are cleared past the caches; those beside the table stay."""
+    tokens, lead = 300, 5
+    r = np.random.default_rng(vocab)
+    ids = r.integers(0, vocab, tokens)
+    ids[:100] = np.arange(100) * 3
+    ids[-1] = vocab - 1
+    whole = r.integers(-8, 9, (tokens, cols))
+    dy = torch.from_numpy(whole).to(DEV).to(torch.bfloat16)
+    buf = torch.full((vocab * cols + 64,), 7.0, device=DEV)
+    out = buf[lead:lead + vocab * cols].view(vocab, cols)
+    S.embed_backward(torch.from_numpy(ids).to(DEV), dy, out, scratch(S.embed_workspace_bytes(tokens, cols)))
+    words, place = np.unique(ids, return_inverse=True)
+    sums = table_of(place, whole, words.size)
+    there = torch.from_numpy(words).to(DEV)
+    assert torch.equal(out[there].double(), sums)
+    out[there] = 0
+    assert (buf[:lead] == 7).all() and (buf[lead + vocab * cols:] == 7).all() and not out.any()
+
+
 # --------------------------------------------------------- log probabilities
 
 
