@@ -669,9 +669,11 @@ scape_status scape_grad_norm(int32_t count, const scape_grad* grads, int32_t gro
  * Clipping by that norm:
  *   out = data * (scale * min(1, max_norm / norm[g]))
  * the product formed in binary64 and rounded from there to out's type; norm
- * [groups] is written as above.  A part whose norm is not
- * finite is scaled and not clipped.  In place, a part with the factor 1 is not
- * written.  max_norm is positive (infinite: scale only).
+ * [groups] is written as above.  A part that holds an infinity or a NaN is
+ * scaled and not clipped; one of finite gradients whose norm only passes fp32's
+ * largest number is clipped by that norm, which norm [groups] gives as infinite.
+ * In place, a part with the factor 1 is not written.  max_norm is positive
+ * (infinite: scale only).
  */
 scape_status scape_grad_clip(int32_t count, const scape_grad* grads, int32_t groups, float scale, float max_norm,
                              float* norm, void* workspace, size_t workspace_bytes, hipStream_t stream);

@@ -978,7 +978,8 @@ def grad_norm(grads: GradList, norm, workspace, scale: float = 1.0, stream=None)
 def clip_grads(grads: GradList, max_norm: float, norm, workspace, scale: float = 1.0, stream=None) -> None:
     """Writes every gradient times scale * min(1, max_norm / its part's norm)
     to its place in out (or its own), and the norms to norm [groups].  A part
-    whose norm is not finite is scaled and not clipped."""
+    that holds an infinity or a NaN is scaled and not clipped (a norm of finite
+    gradients past fp32's largest number clips, and is written as infinite)."""
     g = _grad_list(grads)
     if g.overlap is not None:
         raise ValueError(f"grads[{g.overlap}]: a place that is written overlaps another tensor of the list")

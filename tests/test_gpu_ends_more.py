@@ -67,6 +67,25 @@ def test_clipped_values_are_rounded_once(S, t):
     assert missed > 100  # factors at which a second rounding shows
 
 
+@pytest.mark.parametrize("sizes", [[16], [8, 8], [1] * 200 + [16] * 200])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_clip_by_a_norm_past_fp32(S, sizes, in_place):
+    """Finite gradients whose norm is no fp32 number: clipped by that norm, which
+    is written as infinite.  Beside them a group with an infinity: scaled alone."""
+    grads = [torch.full((n,), 3e38, device=DEV) for n in sizes] + [torch.full((n,), 2.0, device=DEV) for n in sizes]
+    grads[len(sizes)][0] = INF
+    outs = None if in_place else [torch.empty_like(g) for g in grads]
+    gl = S.GradList(grads, out=outs, groups=2)
+    norm = torch.zeros(2, device=DEV)
+    S.clip_grads(gl, 8.0, norm, scratch(S.grad_workspace_bytes(gl)), scale=0.5)
+    got = torch.cat(grads if in_place else outs).double().cpu().numpy()
+    n = sum(sizes)
+    assert norm[0] == INF and norm[1] == INF  # 0.5 x 3e38 x 4 and more
+    want = 8.0 / n ** 0.5
+    assert np.abs(got[:n] - want).max() <= want * 2.0 ** -23  # a rounding, and those of the factor in 64 bits
+    assert got[n] == INF and (got[n + 1:] == 1.0).all()
+
+
 # ----------------------------------------------------------------- embedding
 
 U = 2.0 ** -24
