@@ -9,6 +9,7 @@ library is missing, loading raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional, Tuple
 
@@ -1090,15 +1091,19 @@ class ScapeOptimizer:
 
     def step(self, grads, stream=None, max_norm: Optional[float] = None) -> None:
         t = self.t + 1
-        if self.nonfinite is not None:
-            count_nonfinite(grads, self.nonfinite, self.K * self.n, stream)
-        if max_norm is not None:
-            _need(grads, "grads", self.K * self.n)
+        # what the step would refuse is refused before the gradients are clipped and counted
+        _need_state(self.d, self.params, self.m, self.v, grads, self.e)
+        bias_state_at(self.bt, 0)
+        if not math.isfinite(self.lr):
+            raise ScapeError(1, "lr must be finite")
+        if max_norm is not None and grads is not None:  # no gradients: the step refuses them
             rows = grads.view(-1)[:self.K * self.n].view(self.K, self.n)
             clip_grads(GradList(list(rows), groups=self.K), max_norm, self.grad_norm, self.clip_ws, stream=stream)
+        if self.nonfinite is not None and grads is not None:  # as many as before the clipping, which leaves a row that has one as it is
+            count_nonfinite(grads, self.nonfinite, self.K * self.n, stream)
         step(self.d, self.params, grads, self.m, self.v, self.e, self.mask, self.k, self.bt, self.lr,
              t, self.ws, stream)
-        self.t = t  # a rejected call leaves the step count unchanged
+        self.t = t  # a rejected call leaves the step count, the gradients and their counts unchanged
 
     def place_error_feedback(self, grads, candidates: int = 4, rounds: int = 2) -> dict:
         """Chooses the allocation that holds e (choose_placement): timed

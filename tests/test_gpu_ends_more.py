@@ -262,3 +262,43 @@ def test_grad_list_whose_tensors_moved(S):
     # a new list takes the new memory
     S.clip_grads(S.GradList([a], out=[row]), INF, norm, ws, scale=2.0)
     assert (row == 4).all() and (a == 2).all()
+
+
+# ----------------------------------------------------------------- optimizer
+
+
+def test_refused_step_leaves_the_gradients(S):
+    """A step that is refused for its hyper-parameters, its gradients or its limit
+    has clipped nothing and counted nothing; put right, it is the step it would
+    have been."""
+    from sparse_communication_distributed_amd import workload as W
+    cfg = W.flat_config("refused", 4 * 5000, 4, 2, "0.9")
+    w0 = torch.from_numpy(W.init_params(cfg)).to(DEV)
+    a, b = (S.ScapeOptimizer(w0.clone(), cfg.P, cfg.K, cfg.k, count_nonfinite=True) for _ in range(2))
+    g = torch.from_numpy(W.grads(cfg, 1)).to(DEV)
+    g[1, 3] = INF
+    limit = 0.5 * float(g[0].norm())
+    lr, bt = a.lr, a.bt
+
+    def bad_lr():
+        a.lr = float("nan")
+        a.step(g, max_norm=limit)
+
+    def bad_betas():
+        a.bt = S.betas(0.9, 1.5, 1e-8, 0.0)
+        a.step(g, max_norm=limit)
+
+    before = g.clone()
+    for call in (bad_lr, bad_betas, lambda: a.step(g, max_norm=0.0), lambda: a.step(g, max_norm=float("nan")),
+                 lambda: a.step(g.cpu(), max_norm=limit), lambda: a.step(g[:1].contiguous(), max_norm=limit),
+                 lambda: a.step(g.double(), max_norm=limit), lambda: a.step(None, max_norm=limit)):
+        with pytest.raises((ValueError, S.ScapeError)):
+            call()
+        a.lr, a.bt = lr, bt
+        assert torch.equal(g, before) and a.t == 0 and a.nonfinite_count() == 0 and (a.grad_norm == 0).all()
+    a.step(g, max_norm=limit)
+    assert a.nonfinite_count() == 1 and not torch.equal(g[0], before[0]) and torch.equal(g[1], before[1])
+    g.copy_(before)
+    b.step(g, max_norm=limit)
+    for name in ("params", "m", "v", "e"):
+        assert torch.equal(getattr(a, name).nan_to_num(9.0), getattr(b, name).nan_to_num(9.0)), name
