@@ -1099,7 +1099,8 @@ class ScapeOptimizer:
         if max_norm is not None and grads is not None:  # no gradients: the step refuses them
             rows = grads.view(-1)[:self.K * self.n].view(self.K, self.n)
             clip_grads(GradList(list(rows), groups=self.K), max_norm, self.grad_norm, self.clip_ws, stream=stream)
-        if self.nonfinite is not None and grads is not None:  # as many as before the clipping, which leaves a row that has one as it is
+        if self.nonfinite is not None and grads is not None:
+            # as many as before the clipping, which leaves a row that has one as it is
             count_nonfinite(grads, self.nonfinite, self.K * self.n, stream)
         step(self.d, self.params, grads, self.m, self.v, self.e, self.mask, self.k, self.bt, self.lr,
              t, self.ws, stream)

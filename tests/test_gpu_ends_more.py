@@ -12,6 +12,7 @@ pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
 
 DEV = "cuda:0"
+U = 2.0 ** -24
 INF = float("inf")
 
 
@@ -67,6 +68,48 @@ def test_clipped_values_are_rounded_once(S, t):
     assert missed > 100  # factors at which a second rounding shows
 
 
+@pytest.mark.parametrize("in_place", [True, False])
+def test_clip_of_gradients_whose_squares_fp32_loses(S, in_place):
+    """Subnormal gradients, clipped to a tenth of their norm, and the largest,
+    whose small neighbour is far below them: norm and values within a rounding of
+    the 64-bit ones."""
+    for values, share, scale in (([1e-40, 2e-40, 0.0], 0.1, 0.5), ([1e-30, -3e-30, 2e-31], 0.3, 1.0),
+                                 ([3e38, -3e38, 1e30], 2.0 ** -127, 0.5)):
+        g = torch.tensor(values, device=DEV)
+        v = g.double().cpu().numpy()
+        want = E.grad_norm([v], scale)
+        assert 0 < want < 3.4e38
+        limit = float(np.float32(share * want))
+        out = g if in_place else torch.full_like(g, 7.0)
+        gl = S.GradList([g], out=None if in_place else [out])
+        n = torch.full((1,), -1.0, device=DEV)
+        ws = scratch(S.grad_workspace_bytes(gl))
+        S.grad_norm(gl, n, ws, scale=scale)
+        assert abs(n.item() - want) <= max(want * U * (1 + 1e-6), 2.0 ** -150)
+        n.fill_(-1.0)
+        S.clip_grads(gl, limit, n, ws, scale=scale)
+        assert abs(n.item() - want) <= max(want * U * (1 + 1e-6), 2.0 ** -150)
+        clipped = v * E.clip_factor(want, limit, scale)
+        got = out.double().cpu().numpy()
+        assert (np.abs(got - clipped) <= np.maximum(np.abs(clipped) * U * (1 + 1e-6), 2.0 ** -150)).all(), (got, clipped)
+        assert got[0] != 0
+
+
+def test_grad_norm_of_lists_that_overlap(S):
+    """Lists whose tensors share memory: clipping refuses them, the norm, which
+    only reads, counts each as it is."""
+    buf, other = torch.randn(100, device=DEV), torch.randn(100, device=DEV)
+    a, b, c = buf[:40], buf[40:80], buf[30:50]
+    n, ws = torch.zeros(1, device=DEV), scratch(1 << 16)
+    for gl in (S.GradList([a, a]), S.GradList([a, b, c]), S.GradList([a], out=[buf[1:41]]),
+               S.GradList([buf, other[:4]], out=[other, buf[20:24]])):
+        with pytest.raises(ValueError, match="overlaps another tensor"):
+            S.clip_grads(gl, 1.0, n, ws)
+        S.grad_norm(gl, n, ws)
+        want = E.grad_norm([g.double().cpu().numpy() for g in gl.grads])
+        assert abs(n.item() - want) <= want * U * (1 + 1e-6)
+
+
 @pytest.mark.parametrize("sizes", [[16], [8, 8], [1] * 200 + [16] * 200])
 @pytest.mark.parametrize("in_place", [True, False])
 def test_clip_by_a_norm_past_fp32(S, sizes, in_place):
@@ -87,8 +130,6 @@ def test_clip_by_a_norm_past_fp32(S, sizes, in_place):
 
 
 # ----------------------------------------------------------------- embedding
-
-U = 2.0 ** -24
 
 
 def table_of(ids, dy, vocab):
