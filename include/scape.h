@@ -594,8 +594,10 @@ scape_status scape_embed_backward(int64_t tokens, int64_t vocab, int64_t cols, s
 /* Most alternatives a row of logits can be asked for (64). */
 int32_t scape_token_logprobs_max_top(void);
 
-/* Bytes of scratch scape_token_logprobs needs (256-byte aligned).  0 if a
- * size is invalid. */
+/* Bytes of scratch scape_token_logprobs is given (256-byte aligned).  0 if a
+ * size is invalid.  They are reserved: a row is one workgroup's now, and nothing
+ * is written there; a division of long rows over several would be, in as many
+ * bytes as are asked for then. */
 size_t scape_token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int32_t top);
 
 /*

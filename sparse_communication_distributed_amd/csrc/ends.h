@@ -32,8 +32,8 @@ struct LogprobArgs {
   const float* dentropy;
   scape_matrix dlogits;
 };
-size_t logprobs_workspace(int64_t rows, int64_t vocab, int top);
-hipError_t launch_logprobs(const LogprobArgs& a, void* ws, hipStream_t s);
+constexpr size_t kLogprobsWorkspace = 256;  // reserved: no kernel writes there
+hipError_t launch_logprobs(const LogprobArgs& a, hipStream_t s);
 // The gradient alone, from stats and entropy (inputs here).
 hipError_t launch_logprobs_backward(const LogprobArgs& a, hipStream_t s);
 

@@ -144,7 +144,7 @@ int32_t scape_token_logprobs_max_top(void) { return kMaxTop; }
 
 size_t scape_token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int32_t top) {
   if (!rows_ok(rows) || !cols_ok(vocab) || top < 0 || top > kMaxTop || top > vocab) return 0;
-  return logprobs_workspace(rows, vocab, top);
+  return kLogprobsWorkspace;
 }
 
 scape_status scape_token_logprobs(int64_t rows, int64_t vocab, scape_matrix logits, float scale, scape_ids targets,
@@ -169,8 +169,8 @@ scape_status scape_token_logprobs(int64_t rows, int64_t vocab, scape_matrix logi
   } else if (dlogp || dentropy) {
     return fail(SCAPE_EINVAL, "dlogp and dentropy need dlogits");
   }
-  if ((st = check_workspace(workspace, workspace_bytes, logprobs_workspace(rows, vocab, top)))) return st;
-  return hip_check(launch_logprobs(a, workspace, stream), "token logprobs");
+  if ((st = check_workspace(workspace, workspace_bytes, kLogprobsWorkspace))) return st;
+  return hip_check(launch_logprobs(a, stream), "token logprobs");
 }
 
 scape_status scape_token_logprobs_backward(int64_t rows, int64_t vocab, scape_matrix logits, float scale,

@@ -816,9 +816,7 @@ void run_back(const LogprobArgs& a, bool stream, hipStream_t s) {
 
 }  // namespace
 
-size_t logprobs_workspace(int64_t, int64_t, int) { return 256; }
-
-hipError_t launch_logprobs(const LogprobArgs& a, void*, hipStream_t s) {
+hipError_t launch_logprobs(const LogprobArgs& a, hipStream_t s) {
   if (a.rows == 0) return hipSuccess;
   if (a.logits.dtype == SCAPE_F32) run_type<SCAPE_F32>(a, s);
   else if (a.logits.dtype == SCAPE_BF16) run_type<SCAPE_BF16>(a, s);

@@ -843,7 +843,8 @@ def token_logprobs(logits, targets, logp, workspace, stats=None, entropy=None, t
     top_logp [rows][top], and, where the weights of the log probabilities
     (dlogp [rows]) and entropies (dentropy [rows]) are known before, the
     gradient dlogits (which may be logits itself).  A target outside the
-    vocabulary has logp 0 and no gradient."""
+    vocabulary has logp 0 and no gradient.  The workspace is reserved: checked,
+    and not written."""
     dev = _device_of(logits, "logits")
     rows, vocab = logits.shape
     lists = top_ids if top_ids is not None else top_logp

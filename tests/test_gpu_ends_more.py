@@ -343,3 +343,13 @@ def test_refused_step_leaves_the_gradients(S):
     b.step(g, max_norm=limit)
     for name in ("params", "m", "v", "e"):
         assert torch.equal(getattr(a, name).nan_to_num(9.0), getattr(b, name).nan_to_num(9.0)), name
+
+
+def test_token_logprobs_leaves_its_workspace(S):
+    """The workspace is reserved: two calls at once may share one."""
+    ws = scratch(S.token_logprobs_workspace_bytes(5, 40000, 9))
+    x, y = torch.randn(5, 40000, device=DEV), torch.arange(5, device=DEV)
+    logp, ids = torch.empty(5, device=DEV), torch.empty(5, 9, dtype=torch.int32, device=DEV)
+    w = torch.ones(5, device=DEV)
+    S.token_logprobs(x, y, logp, ws, top_ids=ids, dlogp=w, dlogits=x)
+    assert (ws == 0x5A).all()
