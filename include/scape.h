@@ -623,8 +623,9 @@ size_t scape_token_logprobs_workspace_bytes(int64_t rows, int64_t vocab, int32_t
  * data and ld).  1 <= vocab <= 2^20, 0 <= top <= min(vocab, 64), 2^-100 <=
  * scale <= 2^100.
  *
- * Sums are fp32.  o is summed apart from the 1 it is added to, so logp and
- * entropy keep their relative precision where one word is all but certain.  A
+ * Sums are fp32, of e^t (t = scale (x - m)) to a relative 4 (|t| + 1) 2^-24: t is
+ * fp32 and the exponential a power of 2.  o is summed apart from the 1 it is added
+ * to, so logp and entropy keep this precision where one word is all but certain.  A
  * row whose logits are all -inf has logp and top_logp -inf, entropy 0 and a zero
  * gradient; one that holds a NaN or +inf has NaN for all of them.
  */

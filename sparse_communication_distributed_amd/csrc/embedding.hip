@@ -17,9 +17,9 @@ struct EmbedArgs {
 };
 
 // out[t] = scale * table[ids[t]] + pos_table[pos[t]]: one read and one write,
-// bound by memory: 16384 tokens of 32000 x 2048, fp32 to bf16, 24 us, of which
-// rows read for the first time and out are 117 MB (4.9 TB/s).  `lanes` (a power
-// of two) threads share a token.
+// bound by memory: 16384 tokens of 32000 x 2048, fp32 to bf16, tables that change
+// from pass to pass: 28 us, 81 MB of rows read and 67 written (5.3 TB/s).  `lanes`
+// (a power of two) threads share a token.
 template <int TT, int OT>
 __global__ void __launch_bounds__(kThreads) embed_kernel(EmbedArgs a, int lanes) {
   const int per = kThreads / lanes;
@@ -363,8 +363,9 @@ __device__ __forceinline__ void put_row(const ChunkArgs& a, int64_t w, int64_t c
 }
 
 // Sums the rows of each word of a chunk, and clears rows beside it.  Bound by
-// memory: 16384 tokens of 32000 x 2048 bf16, 56 us, 67 MB of dy, 262 MB of table
-// and partial rows (6 TB/s); without rows to clear it is bound by the latency of
+// memory: 16384 tokens of 32000 x 2048 bf16, inputs and tables that change from
+// pass to pass: 67 us, 66 MB read and 265 written (4.9 TB/s; 56 us over one table
+// that stays in the caches); without rows to clear it is bound by the latency of
 // two loads, a token's number and its row.
 template <int DT, bool WHOLE>
 __global__ void __launch_bounds__(kThreads) embed_chunk_kernel(ChunkArgs a) {
@@ -496,7 +497,7 @@ __device__ __forceinline__ void put_sum(const ChunkArgs& a, uint32_t w, int64_t 
 // A word with many partial rows (only one can begin in the chunks of a
 // workgroup) is shared by all waves, and by the groups of lanes of a wave where
 // a row has fewer than 256 columns, a consecutive part each, joined in a fixed
-// order.  Ordinary words: 6 us for 511 borders of 2048 columns, the latency of
+// order.  Ordinary words: 6.5 us for 511 borders of 2048 columns, the latency of
 // three loads.  65536 tokens of one word, 64 and 1024 columns, all of the call:
 // 114 and 172 us; in four parts, read one after the other, 283 and 201.  (16
 // waves: 114 and 136, but 0.5 to 1 us more for ordinary words.)

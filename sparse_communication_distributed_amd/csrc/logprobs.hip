@@ -558,8 +558,9 @@ __device__ __forceinline__ int64_t load_target(const LogprobArgs& a, int64_t r, 
 }
 
 // With the row in registers.  Bound by memory: 8192 x 32000 bf16 with the
-// gradient 195 us (1.05 GB, 5.4 TB/s), 4096 x 32000 bf16 without 57 us.  One row
-// of 32000 takes 5 us: half of that is arithmetic on one CU.
+// gradient 191 us (1.05 GB, 5.5 TB/s; a pass takes up to 225 where the card comes
+// from idling or waits between launches), 4096 x 32000 bf16 without 60 us.  One
+// row of 32000 takes 5 us: half of that is arithmetic on one CU.
 // (Alternatives take the registers of a second
 // workgroup of a CU: forced into half, 2097 x 32001 bf16 with 20 of them takes 69
 // us instead of 83, but one row 11.2 instead of 9.6.)
@@ -828,7 +829,11 @@ hipError_t launch_logprobs_backward(const LogprobArgs& a, hipStream_t s) {
   if (a.rows == 0) return hipSuccess;
   // What the first call read is still in the caches: past them, dlogits does
   // not drive it out.  1999 x 32000 fp32, both calls: 121 us, without it 152.
-  // (Not so in the call that does both: 8192 x 32000 bf16 191 us, with it 197.)
+  // The call that does both keeps dlogits in the caches, for the products that
+  // read it next: 1024 x 32000 bf16 and one product of it 49.7 us, with stores
+  // past the caches 55.2.  Where it is more than they hold these would win: 8192
+  // x 32000 191 either way alone, with the product 302 and 284; 4096 x 50257 159
+  // and 154, 241 and 236.
   const bool stream = 2 * a.rows * a.vocab * (int64_t)dtype_bytes(a.logits.dtype) > kStreamBytes;
   if (a.logits.dtype == SCAPE_F32) run_back<SCAPE_F32>(a, stream, s);
   else if (a.logits.dtype == SCAPE_BF16) run_back<SCAPE_BF16>(a, stream, s);
